@@ -547,6 +547,90 @@ dsa_status dsa_sparse_attn_prefill_fp8kv(const dsa_cp_local_metadata *md, int32_
                                          const float *attn_sink, float softmax_scale, int32_t H, int32_t D,
                                          int32_t Dv, void *out, dsa_stream_t stream);
 
+/*
+ * 4-bit latent-KV cache: a quarter of the bf16 rows' value bytes, written row
+ * by row into slots as tokens arrive, read back by row number, and attended
+ * over directly (below).  Row of a latent row of D columns, Dv of them values:
+ *   bytes [0, Dv/2)      codes u = c + 8, c in -7..7: of eight columns the even
+ *                        ones in nibbles 0-3 and the odd ones in nibbles 4-7
+ *                        of a little-endian 32-bit word
+ *   then, each from the next multiple of 16 bytes:
+ *   2*(D - Dv) bytes     the rope columns, bf16 as given
+ *   ceil(Dv/16) bytes    one E4M3 scale s per 16 value columns, followed by
+ *   1 byte               e + 127; 255: the row holds a NaN or an infinity
+ *   zero bytes between the sections and up to row_bytes (a multiple of 16; 432
+ *   for D 576, Dv 512)
+ * A value is c * s * 2^e, a bf16 without rounding.  Quantisation, exactly:
+ * e = the least integer with max|x| <= 7 * 448 * 2^e over the row's values,
+ * clamped to -124..114 (an all-zero row: -124); s = E4M3(max|x_b| / 7 / 2^e)
+ * over the block's, to nearest even, at most 448; c = x / (s * 2^e) to the
+ * nearest integer, ties to even, clamped to -7..7 (0 where s = 0).  A row with a
+ * NaN or an infinity among its values stands for NaN in all Dv of them (codes
+ * and scales zero).  Supported: 1 <= Dv <= D <= 65536, Dv and D - Dv multiples
+ * of 8 (else DSA_ERR_SHAPE).
+ */
+/* Host only: bytes of one cache row. */
+dsa_status dsa_kv_int4_row_bytes(int32_t D, int32_t Dv, size_t *bytes);
+
+/* Quantise rows into a cache: row i of kv (bf16, D columns, rows row_stride
+ * elements apart, row_stride >= D and a multiple of 8) becomes cache row
+ * slots[i], or row i where slots is NULL (then num_rows <= num_cache_rows).  A
+ * negative slot leaves its row unwritten; the non-negative slots of a call are
+ * distinct (which of two rows with one slot stays is not defined); a slot at
+ * or beyond num_cache_rows is a DSA_ERR_DEVICE_BOUNDS and is not written.
+ * Cache rows that no slot names keep their bytes.  kv and cache 16-byte
+ * aligned; asynchronous on `stream`. */
+dsa_status dsa_kv_int4_quantize(const void *kv, int64_t row_stride, int32_t num_rows, int32_t D, int32_t Dv,
+                                const int32_t *slots, void *cache, int32_t num_cache_rows, dsa_stream_t stream);
+
+/* Read rows back: kv bf16 [num_rows][D], row i = what cache row rows[i] stands
+ * for, or cache row i where rows is NULL (then num_rows <= num_cache_rows).  A
+ * negative number gives a row of zeros, as does one at or beyond
+ * num_cache_rows, which is a DSA_ERR_DEVICE_BOUNDS; numbers may repeat. */
+dsa_status dsa_kv_int4_dequantize(const void *cache, int32_t num_cache_rows, int32_t D, int32_t Dv,
+                                  const int32_t *rows, int32_t num_rows, void *kv, dsa_stream_t stream);
+
+/* Host only (the current device's SM count enters).  Workspace bytes of
+ * dsa_sparse_attn_int4kv for n queries, 0 where it needs none. */
+dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t topk, size_t *bytes);
+
+/*
+ * MLA sparse attention over the 4-bit cache, for any number of queries down to
+ * a single token, without CP metadata: for query i and head h, over the entries
+ * j of topk_idx[i, :] that name a row,
+ *   l_j = softmax_scale * q[r, h, :] . k_j
+ *   out[r, h, :] = sum_j e^(l_j - m) k_j[:Dv] / (sum_j e^(l_j - m) + e^(sink_h - m))
+ * with k_j what the entry's cache row stands for.
+ *   q          bf16 [num_q_rows][H][D];  out bf16 [num_q_rows][H][Dv]
+ *   q_rows     int32 [n]: row r of q and out that index row i belongs to
+ *              (e.g. local_token_pos of a view: the flat token layout); a
+ *              negative one leaves out as it is; distinct but for those.  NULL:
+ *              r = i (then n <= num_q_rows).  Rows of out that none names keep
+ *              their values.
+ *   topk_idx   int32 [n][topk], any topk >= 1: a negative entry is unused,
+ *              wherever it stands; a row may be named twice and then counts
+ *              twice; a query without a used entry gets zeros
+ *   slots      int32 [num_kv_rows]: entry e names cache row slots[e] (negative:
+ *              unused), for a cache whose rows lie in pages.  NULL: cache row e
+ *   attn_sink  fp32 [H] or NULL
+ *   workspace  at least dsa_sparse_attn_int4kv_workspace_size bytes, 16-byte
+ *              aligned, NULL where that is 0 (else DSA_ERR_WORKSPACE); written
+ *              and read within the call, so calls that may overlap need one each
+ * An entry at or beyond num_kv_rows (num_cache_rows without slots), a slot at or
+ * beyond num_cache_rows and a q_row at or beyond num_q_rows are
+ * DSA_ERR_DEVICE_BOUNDS, and unused.  Only D = 576, Dv = 512 and 1 <= H <= 128
+ * are compiled (DSA_ERR_UNSUPPORTED otherwise).  softmax_scale > 0 and finite.
+ * bf16 products with fp32 sums; softmax in fp32; the two halves of q.k are
+ * exchanged in fp16 (partial sums beyond 65504 saturate).  Few queries are
+ * split over their entries, and the parts joined in a fixed order: the same
+ * inputs give the same bits.
+ */
+dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, const int32_t *q_rows, int32_t n,
+                                  const void *kv_cache, int32_t num_cache_rows, const int32_t *slots,
+                                  int32_t num_kv_rows, const int32_t *topk_idx, int32_t topk,
+                                  const float *attn_sink, float softmax_scale, int32_t H, int32_t D, int32_t Dv,
+                                  void *out, void *workspace, size_t ws_bytes, dsa_stream_t stream);
+
 /* Synchronise `stream`, then return (and clear) the first error a kernel
  * recorded on the current device since the last poll: DSA_OK, or
  * DSA_ERR_DEVICE_TIMEOUT / _BOUNDS / _SEQ_LENS; DSA_ERR_CUDA if the sync
@@ -557,7 +641,10 @@ dsa_status dsa_poll_device_error(dsa_stream_t stream);
  * 3 ints, may be NULL) receives where it was recorded: {site, site detail,
  * linear CTA index}.  Site codes: 11-18 indexer waits, 19-37 attention waits
  * (the detail is the key block), 41-46 bounds checks (indexer slot, top-k
- * slot, top-k overflow, attention slot, attention index, metadata). */
+ * slot, top-k overflow, attention slot, attention index, metadata), 47-51
+ * bounds checks around the 4-bit cache (written slot, row read back, index
+ * entry, its cache row, query row; the detail is the position in the list),
+ * 60-76 waits of the attention over it (the detail is the key block). */
 dsa_status dsa_poll_device_error_detail(dsa_stream_t stream, int32_t *detail);
 
 /* Static string for a status code. */

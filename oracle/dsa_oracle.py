@@ -565,6 +565,101 @@ def kv_fp8_dequantize(cache, D: int, Dv: int) -> np.ndarray:
 
 
 # --------------------------------------------------------------------------
+# 4-bit latent-KV cache
+# --------------------------------------------------------------------------
+# Row: Dv four-bit integers u = c + 8 (of eight columns, the even ones in
+# nibbles 0-3 and the odd ones in nibbles 4-7 of a little-endian 32-bit word),
+# the D - Dv rope columns as bf16, one E4M3 scale per 16 value columns, one
+# byte e + 127 (255: NaN row); the first three sections start on multiples of
+# 16 bytes, zero bytes elsewhere.  A value is c * scale * 2^e.
+
+INT4_BLOCK = 16
+INT4_E_MIN, INT4_E_MAX = -124, 114
+
+
+def kv_int4_layout(D: int, Dv: int) -> tuple:
+    """(rope, scales, exponent, row_bytes): byte offsets and the row's bytes."""
+    up = lambda n: -(-n // 16) * 16
+    rope = up(Dv // 2)
+    scales = rope + up(2 * (D - Dv))
+    exponent = scales + -(-Dv // INT4_BLOCK)
+    return rope, scales, exponent, up(exponent + 1)
+
+
+def kv_int4_nibbles(Dv: int) -> np.ndarray:
+    """The nibble (low one of byte 0 first) that holds each column's code."""
+    c = np.arange(Dv)
+    return c // 8 * 8 + (c % 8) // 2 + 4 * (c % 2)
+
+
+def kv_int4_quantize(kv, Dv: int) -> np.ndarray:
+    """bf16-valued latent rows kv [R, D] -> cache bytes, in exact arithmetic:
+    every quotient that could meet a border between two codes is taken in
+    float64, where such borders (half integers, E4M3 midpoints) are met
+    exactly and everything else stays at least 2^-8 of itself away."""
+    x = np.asarray(kv, dtype=np.float64)
+    R, D = x.shape
+    rope, scales, exponent, row_bytes = kv_int4_layout(D, Dv)
+    out = np.zeros((R, row_bytes), dtype=np.uint8)
+    nib = kv_int4_nibbles(Dv)
+    for r in range(R):
+        v = x[r, :Dv]
+        good = bool(np.isfinite(v).all())
+        v = v if good else np.zeros(Dv)
+        top = np.abs(v).max()
+        e = INT4_E_MIN
+        while top > 7 * 448 * 2.0 ** e and e < INT4_E_MAX:
+            e += 1
+        codes = np.zeros(Dv, dtype=np.int64)
+        for b in range(0, Dv, INT4_BLOCK):
+            y = v[b:b + INT4_BLOCK] / 2.0 ** e
+            byte = int(e4m3_encode(np.abs(y).max() / 7))
+            s = float(e4m3_decode(byte))
+            out[r, scales + b // INT4_BLOCK] = byte
+            if s > 0:
+                codes[b:b + INT4_BLOCK] = np.clip(np.rint(y / s), -7, 7)
+        u = np.zeros(Dv, dtype=np.uint8)
+        u[nib] = codes + 8
+        out[r, :Dv // 2] = u[0::2] | (u[1::2] << 4)
+        out[r, exponent] = e + 127 if good else 255
+    bits = np.asarray(kv, dtype=np.float32)[:, Dv:].copy().view(np.uint32) >> 16
+    out[:, rope:rope + 2 * (D - Dv)] = bits.astype(np.uint16).view(np.uint8).reshape(R, 2 * (D - Dv))
+    return out
+
+
+def kv_int4_dequantize(cache, D: int, Dv: int) -> np.ndarray:
+    """Cache bytes [R, row_bytes] -> the latent rows [R, D] as float64."""
+    b = np.asarray(cache, dtype=np.uint8)
+    R = b.shape[0]
+    rope, scales, exponent, _ = kv_int4_layout(D, Dv)
+    nib = kv_int4_nibbles(Dv)
+    code = (b[:, nib // 2] >> (4 * (nib % 2)).astype(np.uint8) & 15).astype(np.float64) - 8
+    e = b[:, exponent].astype(np.float64)
+    step = np.where(e == 255, np.nan, np.exp2(e - 127))
+    val = code * e4m3_decode(b[:, scales + np.arange(Dv) // INT4_BLOCK]) * step[:, None]
+    tail = np.ascontiguousarray(b[:, rope:rope + 2 * (D - Dv)]).view(np.uint16).astype(np.uint32) << 16
+    return np.concatenate([val, tail.view(np.float32).astype(np.float64)], axis=1)
+
+
+def sparse_attention_entries(q, rows, idx, scale: float, Dv: int, sink=None, slots=None) -> np.ndarray:
+    """sparse_attention of every query over the entries of its index row that
+    name a row: q [n, H, D], rows [R, D], idx [n, topk] (negative: unused),
+    slots [num_kv_rows] (entry -> row, negative: unused) or None -> [n, H, Dv];
+    zeros for a query without a used entry."""
+    n, H = np.asarray(q).shape[:2]
+    out = np.zeros((n, H, Dv))
+    for i in range(n):
+        pick = np.asarray(idx[i])
+        pick = pick[pick >= 0]
+        if slots is not None:
+            pick = np.asarray(slots)[pick]
+            pick = pick[pick >= 0]
+        if pick.size:
+            out[i] = sparse_attention(q[i], rows[pick], scale, Dv, sink)
+    return out
+
+
+# --------------------------------------------------------------------------
 # FP8 indexer operands (R19)
 # --------------------------------------------------------------------------
 

@@ -26,7 +26,8 @@ __all__ = [
     "dsa_indexer_topk_rows", "dsa_indexer_scores", "dsa_indexer_fp8_rows", "dsa_indexer_topk_fp8", "dsa_indexer_scores_fp8",
     "dsa_sparse_attn_prefill", "dsa_sparse_attn_prefill_headsharded", "dsa_sparse_attn_prefill_rows",
     "dsa_swa_index",
-    "dsa_sparse_attn_prefill_swa", "dsa_poll_device_error",
+    "dsa_sparse_attn_prefill_swa", "dsa_kv_int4_row_bytes", "dsa_kv_int4_quantize", "dsa_kv_int4_dequantize",
+    "dsa_sparse_attn_int4kv_workspace_size", "dsa_sparse_attn_int4kv", "dsa_poll_device_error",
 ]
 
 
@@ -592,6 +593,178 @@ def dsa_kv_fp8_dequantize(cache: torch.Tensor, D: int, Dv: int, out: torch.Tenso
     if tuple(out.shape) != (R, D):
         raise ValueError(f"out must be [{R}, {D}]")
     check(load().dsa_kv_fp8_dequantize(_ptr(cache), R, D, Dv, _ptr(out), _stream(stream)), "dsa_kv_fp8_dequantize")
+    return out
+
+
+def _same_device(*tensors) -> torch.device:
+    """The one CUDA device of the given tensors (None skipped)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if dev is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
+        dev = t.device
+    return dev
+
+
+class _launch_on:
+    """Make ``dev`` current and ``stream`` (or the device's current stream)
+    the current stream for the calls and allocations of the block: a tensor
+    allocated there belongs to the stream its kernel runs on."""
+
+    def __init__(self, dev: torch.device, stream):
+        self.ctx = []
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            if stream != torch.cuda.current_stream(dev) or dev.index != torch.cuda.current_device():
+                self.ctx.append(torch.cuda.stream(stream))
+        elif dev.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(dev))
+        self.dev = dev
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return C.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+        return False
+
+
+def dsa_kv_int4_row_bytes(D: int, Dv: int) -> int:
+    """Bytes of one 4-bit latent-KV cache row (include/dsa_cp.h)."""
+    n = C.c_size_t()
+    check(load().dsa_kv_int4_row_bytes(D, Dv, C.byref(n)), "dsa_kv_int4_row_bytes")
+    return n.value
+
+
+def dsa_kv_int4_quantize(kv: torch.Tensor, Dv: int, out: torch.Tensor | None = None,
+                         slots: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Latent rows kv bf16 [n, D] -> 4-bit cache rows.  Without ``out`` a new
+    cache uint8 [n, row_bytes]; with ``out`` [R, row_bytes], row i is written
+    at ``slots``[i] (int32 [n], distinct, negative: not written; without
+    ``slots`` at row i) and the other rows keep their bytes.  The rows of kv
+    may lie apart (a slice of the columns of a wider tensor), each starting
+    on a 16-byte boundary."""
+    if not isinstance(kv, torch.Tensor) or not kv.is_cuda or kv.dtype != torch.bfloat16 or kv.dim() != 2:
+        raise ValueError("kv must be a CUDA bfloat16 tensor [n, D]")
+    n, D = kv.shape
+    rb = dsa_kv_int4_row_bytes(D, Dv)
+    stride = kv.stride(0) if n > 1 else D
+    if kv.stride(1) != 1 or stride < D or stride % 8 or kv.data_ptr() % 16:
+        raise ValueError("the rows of kv must be contiguous, not overlap and start on 16-byte boundaries")
+    if slots is not None:
+        _need(slots, torch.int32, "slots")
+        if tuple(slots.shape) != (n,):
+            raise ValueError(f"slots must be [{n}]")
+        if out is None:
+            raise ValueError("slots need the cache they number (out)")
+    if out is not None:
+        _need(out, torch.uint8, "out")
+        if out.dim() != 2 or out.shape[1] != rb or (slots is None and out.shape[0] < n):
+            raise ValueError(f"out must be [R, {rb}] with a row for every row written")
+    with _launch_on(_same_device(kv, out, slots), stream) as st:
+        if out is None:
+            out = torch.empty((n, rb), dtype=torch.uint8, device=kv.device)
+        check(load().dsa_kv_int4_quantize(_ptr(kv), stride, n, D, Dv, _ptr(slots), _ptr(out), out.shape[0], st),
+              "dsa_kv_int4_quantize")
+    return out
+
+
+def dsa_kv_int4_dequantize(cache: torch.Tensor, D: int, Dv: int, rows: torch.Tensor | None = None,
+                           out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """4-bit cache uint8 [R, row_bytes] -> the bf16 rows it stands for: all of
+    them [R, D], or those numbered by ``rows`` (int32 [n], negative: a row of
+    zeros) [n, D]."""
+    _need(cache, torch.uint8, "cache")
+    if cache.dim() != 2 or cache.shape[1] != dsa_kv_int4_row_bytes(D, Dv):
+        raise ValueError("cache rows do not have the 4-bit row size of (D, Dv)")
+    n = cache.shape[0]
+    if rows is not None:
+        _need(rows, torch.int32, "rows")
+        if rows.dim() != 1:
+            raise ValueError("rows must be [n]")
+        n = rows.shape[0]
+    if out is not None:
+        _need(out, torch.bfloat16, "out")
+        if tuple(out.shape) != (n, D):
+            raise ValueError(f"out must be [{n}, {D}]")
+    with _launch_on(_same_device(cache, rows, out), stream) as st:
+        if out is None:
+            out = torch.empty((n, D), dtype=torch.bfloat16, device=cache.device)
+        check(load().dsa_kv_int4_dequantize(_ptr(cache), cache.shape[0], D, Dv, _ptr(rows), n, _ptr(out), st),
+              "dsa_kv_int4_dequantize")
+    return out
+
+
+def dsa_sparse_attn_int4kv_workspace_size(n: int, H: int, topk: int) -> int:
+    """Workspace bytes of dsa_sparse_attn_int4kv for ``n`` queries on the current device."""
+    b = C.c_size_t()
+    check(load().dsa_sparse_attn_int4kv_workspace_size(n, H, topk, C.byref(b)), "dsa_sparse_attn_int4kv_workspace_size")
+    return b.value
+
+
+def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: torch.Tensor, softmax_scale: float,
+                           Dv: int, attn_sink: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                           q_rows: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The sparse attention over a 4-bit cache uint8 [R, row_bytes], for any
+    number of queries down to one token: q bf16 [m, H, D], topk_idx int32
+    [n, topk] (negative entries unused) -> bf16 [m, H, Dv].  Entry e names
+    cache row e, or cache row ``slots``[e] (int32 [num_kv_rows]).  Index row i
+    belongs to q row i (n = m), or to row ``q_rows``[i] (int32 [n], distinct
+    but for negative ones, which have none); rows of ``out`` that none names
+    keep their values, so q_rows needs ``out``.  ``workspace``: uint8, at
+    least dsa_sparse_attn_int4kv_workspace_size bytes, allocated per call
+    when omitted."""
+    _need(q, torch.bfloat16, "q")
+    _need(kv_cache, torch.uint8, "kv_cache")
+    _need(topk_idx, torch.int32, "topk_idx")
+    if q.dim() != 3 or topk_idx.dim() != 2:
+        raise ValueError("q must be [m, H, D] and topk_idx [n, topk]")
+    m, H, D = q.shape
+    n, topk = topk_idx.shape
+    if kv_cache.dim() != 2 or kv_cache.shape[1] != dsa_kv_int4_row_bytes(D, Dv):
+        raise ValueError("q / kv_cache do not match (D, Dv)")
+    if attn_sink is not None:
+        _need(attn_sink, torch.float32, "attn_sink")
+        if tuple(attn_sink.shape) != (H,):
+            raise ValueError(f"attn_sink must be [{H}]")
+    if slots is not None:
+        _need(slots, torch.int32, "slots")
+        if slots.dim() != 1:
+            raise ValueError("slots must be [num_kv_rows]")
+    if q_rows is None:
+        if n != m:
+            raise ValueError("q and topk_idx must have the same number of rows (or pass q_rows)")
+    else:
+        _need(q_rows, torch.int32, "q_rows")
+        if tuple(q_rows.shape) != (n,):
+            raise ValueError(f"q_rows must be [{n}]")
+        if out is None:
+            raise ValueError("q_rows need the out tensor whose other rows stay")
+    if out is not None:
+        _need(out, torch.bfloat16, "out")
+        if tuple(out.shape) != (m, H, Dv):
+            raise ValueError(f"out must be [{m}, {H}, {Dv}]")
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    dev = _same_device(q, kv_cache, topk_idx, attn_sink, slots, q_rows, out, workspace)
+    with _launch_on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((m, H, Dv), dtype=torch.bfloat16, device=dev)
+        if workspace is None:
+            size = dsa_sparse_attn_int4kv_workspace_size(n, H, topk)
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+        check(load().dsa_sparse_attn_int4kv(_ptr(q), m, _ptr(q_rows), n, _ptr(kv_cache), kv_cache.shape[0],
+                                            _ptr(slots), 0 if slots is None else slots.shape[0], _ptr(topk_idx), topk,
+                                            _ptr(attn_sink), float(softmax_scale), H, D, Dv, _ptr(out),
+                                            _ptr(workspace), 0 if workspace is None else workspace.numel(), st),
+              "dsa_sparse_attn_int4kv")
     return out
 
 

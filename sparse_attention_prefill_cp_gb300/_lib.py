@@ -89,6 +89,16 @@ SIGNATURES = {
     "dsa_kv_fp8_row_bytes": (C.c_int, [C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
     "dsa_kv_fp8_quantize": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, c_stream]),
     "dsa_kv_fp8_dequantize": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, c_stream]),
+    "dsa_kv_int4_row_bytes": (C.c_int, [C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
+    "dsa_kv_int4_quantize": (C.c_int, [C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
+                                       C.c_int32, c_stream]),
+    "dsa_kv_int4_dequantize": (C.c_int, [C.c_void_p, C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_int32,
+                                         C.c_void_p, c_stream]),
+    "dsa_sparse_attn_int4kv_workspace_size": (C.c_int, [C.c_int32, C.c_int32, C.c_int32, C.POINTER(C.c_size_t)]),
+    "dsa_sparse_attn_int4kv": (C.c_int, [C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p, C.c_int32,
+                                         C.c_void_p, C.c_int32, C.c_void_p, C.c_int32, C.c_void_p, C.c_float,
+                                         C.c_int32, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_size_t,
+                                         c_stream]),
     "dsa_poll_device_error": (C.c_int, [c_stream]),
     "dsa_poll_device_error_detail": (C.c_int, [c_stream, c_i32p]),
     "dsa_status_string": (C.c_char_p, [C.c_int]),

@@ -1,0 +1,790 @@
+// MLA sparse attention over the 4-bit latent-KV cache (row format:
+// int4_common.cuh), for any number of queries down to one token:
+//   l_j = softmax_scale * q[i, h, :] . k_j,  k_j the row that entry j selects
+//   out[i, h, :] = sum_j e^(l_j - m) k_j[:Dv] / (sum_j e^(l_j - m) + e^(sink_h - m))
+// over the entries of the query's index row that name a row; the others are
+// masked wherever they stand, and a query with none gets zeros.
+//
+// One 2-CTA cluster per query and split of its entries, D = 576, Dv = 512, up
+// to 128 heads (the rows of the M = 128 MMA; missing heads are zero rows).
+// One fp32 accumulator of 128 heads x 512 values would fill an SM's tensor
+// memory, so CTA c owns value columns [256c, 256c + 256) and computes the
+// partial QK over latent dims [256c, 256c + 256) + [512 + 32c, 512 + 32c + 32):
+// each CTA decodes its half of a row once, and one shared-memory tile serves
+// as QK's K-major B and PV's MN-major B.  The pair exchanges partial S tiles
+// through distributed shared memory, in fp16: a bulk copy of 16 KB each way
+// and block is what the links carry in a block's time (13.6 B/clk measured,
+// 32 KB of fp32 would take 2,400 cycles of it); the rounding is 2^-12 of a
+// partial sum of q.k, a few 1e-4 in the logit for logits of unit size, and
+// below the 2^-9 of P's bf16.  P is bf16 for the MMA; statistics, sums and O
+// are fp32.  A partial sum beyond 65504 saturates there.
+//
+// Tensor memory (512 columns): O (256), two S buffers (2 x 64), the CTA's 256
+// main Q dims as bf16 (128).  16 warps: 0-7 softmax in two warpgroups (one
+// head row = one TMEM lane per thread; warpgroup w owns columns [32w, 32w + 32)
+// of every block of 64 entries), 8 TMA for Q then MMA issue, 9 the exchange
+// agent, 10-15 the gather: two warps per block, three blocks in flight.
+//
+// The gather reads a row's codes, scales and exponent, decodes to bf16 with
+// one shift, one LOP3 and one packed fma per two values (no conversion
+// instructions: those share a pipe with the softmax's packing) and stores into
+// the swizzled tiles.  Index entries and slots are fetched two and one turns
+// ahead of the block that needs them.
+//
+// Splits: with few queries each query's entries are divided among several
+// clusters, which leave unnormalised fp32 O halves and (m, l) per head in the
+// workspace; a second kernel joins them in split order (no atomics, so the
+// result does not depend on timing).
+#include "int4_common.cuh"
+#include "internal.h"
+
+namespace dsa {
+namespace {
+
+constexpr int kD = 576, kDv = 512;
+constexpr int kHeads = 128;          // M of the MMAs
+constexpr int kBN = 64;              // entries per block
+constexpr int kHalf = kBN / 2;       // columns per softmax warpgroup
+constexpr int kStages = 4;
+constexpr int kNMain = 4;            // 64-wide latent chunks per CTA (128B swizzle), plus one of 32 (64B swizzle)
+constexpr int kDvc = 256;            // value columns per CTA
+constexpr int kThreads = 512;
+constexpr int kQMain = kNMain * 128 * 128, kQTail = 128 * 64;
+constexpr int kStageMain = kNMain * kBN * 128, kStageBytes = kStageMain + kBN * 64;
+constexpr int kQKMainSteps = kNMain * 4, kQKSteps = kQKMainSteps + 2, kPVSteps = kBN / 16;
+constexpr int kSCol = kDvc, kQCol = kSCol + 2 * kBN, kTmemCols = 512;
+constexpr int kRecvBytes = 128 * kBN * 2;  // one partial-S tile (fp16), rows swizzled; P (bf16) overwrites it
+constexpr int kOffStage = 0;
+constexpr int kOffQStage = kOffStage + kStageBytes;  // Q main staged in stages 1..2 at start
+constexpr int kOffQTail = kOffStage + kStages * kStageBytes;
+constexpr int kOffRecv = kOffQTail + kQTail;
+constexpr int kOffStg = kOffRecv + 2 * kRecvBytes;
+constexpr int kOffRed = kOffStg + 2 * kRecvBytes;     // [3][2 warpgroups][128] floats
+constexpr int kOffBar = kOffRed + 3 * 2 * 128 * 4;
+constexpr int kNumBars = 2 + 2 * kStages + 2 * 9 + 2;
+constexpr int kOffMisc = kOffBar + kNumBars * 8;      // [0] tmem, [4..19] last used entry per warp, [20..27] masks
+constexpr int kSmemBytes = kOffMisc + 28 * 4 + 1024;
+constexpr uint32_t kIdescQK = idesc_bf16(128, kBN, false, false);
+constexpr uint32_t kIdescPV = idesc_bf16(128, kDvc, false, true);
+static_assert(kQCol + kNMain * 32 <= kTmemCols, "TMEM budget");
+static_assert(kQMain <= 2 * kStageBytes, "Q staging fits in stages 1..2");
+static_assert(kStageBytes % 1024 == 0 && kOffQTail % 1024 == 0 && kOffRecv % 1024 == 0, "alignment");
+static_assert(kHeads * kDvc * 4 <= kStages * kStageBytes, "the fp32 O half fits in the stages");
+static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+struct AttnInt4Params {
+  const uint8_t *cache;    // [cache_rows][row_bytes]
+  const int32_t *slots;    // [num_kv_rows] KV row -> cache row (negative: no row), or nullptr: entries are cache rows
+  const int32_t *idx;      // [n][topk]
+  const int32_t *q_rows;   // [n] row of q and out (negative: none), or nullptr: row i
+  const float *sink;       // [H] or nullptr
+  __nv_bfloat16 *out;      // [num_q_rows][H][Dv]
+  float *part_o;           // [n * splits][2][H][256], 16-byte units swizzled (splits > 1)
+  float2 *part_ml;         // [n * splits][2][H] (splits > 1)
+  float scale_log2;        // softmax_scale * log2(e)
+  int32_t H, topk, splits, split_len;  // split_len: entries per split, a multiple of kBN
+  int32_t num_kv_rows, cache_rows, num_q_rows;
+  Int4Geom g;
+  int *err;
+};
+
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Multiply TMEM columns [c0, c1) of the warp's lanes by alpha.  Out of line:
+// it runs only when a row's max grows by more than 2^8.  Warp-collective.
+__device__ __noinline__ void scale_o(uint32_t lane_base, int c0, int c1, float alpha) {
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    uint32_t r[32];
+    tmem_ld32(lane_base + c, r);
+    tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha);
+    tmem_st32(lane_base + c, r);
+  }
+  tmem_st_wait();
+}
+
+// The cache row that an index entry names, -1 where it names none.
+__device__ __forceinline__ int resolve(const AttnInt4Params &P, int entry, int k) {
+  if (entry < 0) return -1;
+  int row = entry;
+  if (P.slots) {
+    if (entry >= P.num_kv_rows) {
+      record_error(P.err, DSA_ERR_DEVICE_BOUNDS, 49, k);
+      return -1;
+    }
+    row = __ldg(P.slots + entry);
+    if (row < 0) return -1;
+  }
+  if (row >= P.cache_rows) {
+    record_error(P.err, DSA_ERR_DEVICE_BOUNDS, 50, k);
+    return -1;
+  }
+  return row;
+}
+
+// The bulk copy of an O half out of shared memory.
+__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    sparse_attn_int4_kernel(const __grid_constant__ CUtensorMap qmain_map, const __grid_constant__ CUtensorMap qtail_map,
+                            const AttnInt4Params P) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
+  uint64_t *q_full = bars;                  // Q staged + tail landed (TMA)
+  uint64_t *q_ready = bars + 1;             // Q main copied into TMEM, staging free (8 softmax warps)
+  uint64_t *kv_full = bars + 2;             // [kStages] rows decoded (64 gather threads)
+  uint64_t *kv_empty = kv_full + kStages;   // [kStages] PV done with the stage (MMA commit)
+  uint64_t *s_full = kv_empty + kStages;    // [2] QK done (MMA commit)
+  uint64_t *s_free = s_full + 2;            // [2] S read out of TMEM (8 softmax warps)
+  uint64_t *p_full = s_free + 2;            // [2] P tile written (8 softmax warps)
+  uint64_t *pv_done = p_full + 2;           // [2] PV done, its P tile free (MMA commit)
+  uint64_t *recv_full = pv_done + 2;        // [2] the peer's partial S landed (bulk copy)
+  uint64_t *recv_empty = recv_full + 2;     // [2] the peer is done with what we sent (peer's agent)
+  uint64_t *red_full = recv_empty + 2;      // [2] both warpgroups' block maxima written (8 warps)
+  uint64_t *staged = red_full + 2;          // [2] our partial-S tile written (8 softmax warps)
+  uint64_t *stg_free = staged + 2;          // [2] the bulk copy has read our tile (sender)
+  uint64_t *fin_full = stg_free + 2;        // both warpgroups' denominators written (8 warps)
+  uint64_t *o_staged = fin_full + 1;        // O rows staged in smem (8 warps)
+  int32_t *misc = reinterpret_cast<int32_t *>(smem + kOffMisc);
+  int32_t *last_used = misc + 4;
+  uint32_t *masks = reinterpret_cast<uint32_t *>(misc + 20);  // [kStages][2]: bit r of word w = row 32w + r is used
+  float *red = reinterpret_cast<float *>(smem + kOffRed);
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t crank = cluster_ctarank(), peer = crank ^ 1u;
+  const int unit = static_cast<int>(blockIdx.x >> 1);  // query * splits + split
+  const int query = unit / P.splits;
+  const int k0 = (unit - query * P.splits) * P.split_len;
+  const int k1 = min(P.topk, k0 + P.split_len);
+  const int main_dim0 = static_cast<int>(crank) * kDvc;
+  const int tail_dim0 = kDv + 32 * static_cast<int>(crank);
+  const int32_t *idx_row = P.idx + static_cast<int64_t>(query) * P.topk;
+  int qrow = P.q_rows ? P.q_rows[query] : query;
+  if (qrow >= P.num_q_rows) {
+    if (tid == 0) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, 51, query);
+    qrow = -1;
+  }
+
+  // Q's TMA first: its latency overlaps the scan of the index row and the set-up
+  const bool q_issued = qrow >= 0;
+  if (tid == 256) {  // warp 8, lane 0
+    mbar_init(q_full, 1);
+    fence_mbar_init();
+    if (q_issued) {
+      tma_prefetch_desc(&qmain_map);
+      mbar_arrive_expect_tx(q_full, kQMain + kQTail);
+      for (int i = 0; i < kNMain; ++i)
+        tma_load_3d(smem + kOffQStage + i * 16384, &qmain_map, main_dim0 + 64 * i, 0, qrow, q_full);
+      tma_load_3d(smem + kOffQTail, &qtail_map, tail_dim0, 0, qrow, q_full);
+    }
+  }
+  if (tid == 0) {
+    mbar_init(q_ready, 8);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&kv_full[s], 64);
+      mbar_init(&kv_empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&s_free[b], 8);
+      mbar_init(&p_full[b], 8);
+      mbar_init(&pv_done[b], 1);
+      mbar_init(&recv_full[b], 1);
+      mbar_init(&recv_empty[b], 1);
+      mbar_init(&red_full[b], 8);
+      mbar_init(&staged[b], 8);
+      mbar_init(&stg_free[b], 1);
+    }
+    mbar_init(fin_full, 8);
+    mbar_init(o_staged, 8);
+    fence_mbar_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), kTmemCols);
+    tmem_relinquish();
+  }
+  // one past the split's last entry that names a row: the blocks behind it are skipped
+  int last = 0;
+  if (q_issued)
+    for (int k = k0 + tid; k < k1; k += kThreads)
+      if (__ldg(idx_row + k) >= 0) last = k + 1 - k0;
+  last = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(last)));
+  if (lane == 0) last_used[warp] = last;
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) last = max(last, last_used[i]);
+
+  const uint32_t tmem = static_cast<uint32_t>(misc[0]);
+  const int nb = (last + kBN - 1) / kBN;
+  const int64_t half = static_cast<int64_t>(unit) * 2 + crank;  // of the workspace arrays
+  __nv_bfloat16 *out_row = P.out + static_cast<int64_t>(qrow) * P.H * kDv + main_dim0;
+
+  if (nb == 0) {
+    if (P.splits > 1) {
+      if (tid < P.H) P.part_ml[half * P.H + tid] = make_float2(-__builtin_huge_valf(), 0.f);
+    } else if (qrow >= 0) {
+      for (int u = tid; u < P.H * (kDvc / 8); u += kThreads)
+        *reinterpret_cast<uint4 *>(out_row + static_cast<int64_t>(u / (kDvc / 8)) * kDv + u % (kDvc / 8) * 8) =
+            make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (q_issued) mbar_wait(q_full, 0, P.err, 60);  // the Q load issued at the start has landed
+  } else if (warp == 8) {
+    if (lane == 0) {
+      // ---------------- MMA issuer, event-driven: QK(j) as soon as its rows are
+      // there, its S buffer is free and PV(j - 3) has been issued, PV(i) as
+      // soon as P(i) is written; each stream in order
+      const uint32_t st_addr = smem_u32(smem + kOffStage);
+      const uint64_t qk_b0 = smem_desc(st_addr, 16, 1024, kLayoutSW128);
+      const uint64_t qk_t0 = smem_desc(st_addr + kStageMain, 16, 512, kLayoutSW64);
+      const uint64_t qt_a0 = smem_desc(smem_u32(smem + kOffQTail), 16, 512, kLayoutSW64);
+      const uint64_t pv_a0 = smem_desc(smem_u32(smem + kOffRecv), 16, 1024, kLayoutSW128);
+      const uint64_t pv_b0 = smem_desc(st_addr, kBN * 128, 1024, kLayoutSW128);
+      const uint32_t s_tm = tmem + kSCol, q_tm = tmem + kQCol;
+      bool ok = mbar_wait(q_full, 0, P.err, 61) && mbar_wait(q_ready, 0, P.err, 61);
+      tc_fence_after();
+      int qk = 0, pv = 0;
+      long long t_prog = clock64(), t_check = t_prog;
+      while (ok && pv < nb) {
+        bool progressed = false;
+        if (qk < nb && qk < pv + 3 && mbar_test(&kv_full[qk % kStages], (qk / kStages) & 1) &&
+            (qk < 2 || mbar_test(&s_free[qk & 1], ((qk - 2) >> 1) & 1))) {
+          tc_fence_after();
+          const uint32_t d = s_tm + (qk & 1) * kBN;
+          const uint32_t so = static_cast<uint32_t>((qk % kStages) * kStageBytes) >> 4;
+          const uint64_t kb = desc_add(qk_b0, so), kt = desc_add(qk_t0, so);
+#pragma unroll
+          for (int k = 0; k < kQKSteps; ++k) {
+            if (k < kQKMainSteps) {
+              const int i = k >> 2, sub = k & 3;
+              mma_ts(d, q_tm + k * 8, desc_add(kb, (i * (kBN * 128) + sub * 32) >> 4), kIdescQK, k > 0 ? 1u : 0u);
+            } else {
+              const int t = k - kQKMainSteps;
+              mma_ss(d, desc_add(qt_a0, t * 2), desc_add(kt, t * 2), kIdescQK, 1u);
+            }
+          }
+          mma_commit(&s_full[qk & 1]);
+          ++qk;
+          progressed = true;
+        }
+        if (pv < qk && mbar_test(&p_full[pv & 1], (pv >> 1) & 1)) {
+          tc_fence_after();
+          const int bi = pv & 1, si = pv % kStages;
+          const uint64_t vb = desc_add(pv_b0, static_cast<uint32_t>(si * kStageBytes) >> 4);
+          const uint64_t pb = desc_add(pv_a0, static_cast<uint32_t>(bi * kRecvBytes) >> 4);
+#pragma unroll
+          for (int k = 0; k < kPVSteps; ++k)
+            mma_ss(tmem, desc_add(pb, k * 2), desc_add(vb, k * 128), kIdescPV, (pv > 0 || k > 0) ? 1u : 0u);
+          mma_commit(&pv_done[bi]);
+          mma_commit(&kv_empty[si]);
+          ++pv;
+          progressed = true;
+        }
+        const long long now = clock64();
+        if (progressed) {
+          t_prog = now;
+        } else if (now - t_check > 100000) {
+          t_check = now;
+          if (error_set(P.err)) {
+            ok = false;
+          } else if (now - t_prog > kWaitLimitCycles) {
+            record_error(P.err, DSA_ERR_DEVICE_TIMEOUT, 62, qk * 10000 + pv);
+            ok = false;
+          }
+        }
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ---------------- exchange agent: ships each staged partial-S tile to the
+      // peer with one bulk copy, and tells the peer when its tiles have been read
+      const uint32_t peer_recv = map_to_cta(smem_u32(smem + kOffRecv), peer);
+      const uint32_t peer_full = map_to_cta(smem_u32(recv_full), peer);
+      bool ok = true;
+      for (int t = 0; ok && t <= nb; ++t) {
+        if (t < nb) {
+          const int b = t & 1;
+          if (!(ok = mbar_wait(&staged[b], (t >> 1) & 1, P.err, 63, t))) break;
+          if (t >= 2 && !(ok = mbar_wait<true>(&recv_empty[b], ((t >> 1) & 1) ^ 1, P.err, 64, t))) break;
+          bulk_copy_to_peer(peer_recv + b * kRecvBytes, smem + kOffStg + b * kRecvBytes, kRecvBytes, peer_full + b * 8);
+          bulk_commit();
+          bulk_wait_read0();
+          mbar_arrive(&stg_free[b]);
+        }
+        if (t >= 1) {
+          const int b = (t - 1) & 1;
+          // PV(t-1) has read P(t-1), which sits in the tile the peer filled
+          if (!(ok = mbar_wait(&pv_done[b], ((t - 1) >> 1) & 1, P.err, 65, t - 1))) break;
+          mbar_arrive_remote_relaxed(&recv_empty[b], peer);
+        }
+      }
+      bulk_wait_read0();
+    }
+  } else if (warp >= 10) {
+    // ---------------- gather: warps 10 + 2g and 11 + 2g take the blocks
+    // j = g (mod 3), warp w of them rows 32w .. 32w + 31.  Lane l knows row
+    // 32w + l of the block; to decode, eight lanes take one row, lane v of them
+    // unit v (8 columns) of each of the CTA's four 64-column chunks, so the
+    // stores of eight lanes fall on eight different bank groups.
+    constexpr int kGroups = 3;
+    const int g = (warp - 10) >> 1, w = (warp - 10) & 1;
+    const int v = lane & 7, r4 = lane >> 3;
+    auto entry_of = [&](int j) {
+      const int k = j * kBN + 32 * w + lane;
+      return j < nb && k < last ? __ldg(idx_row + k0 + k) : -1;
+    };
+    int entry = entry_of(g);
+    int row = resolve(P, entry, k0 + g * kBN + 32 * w + lane);
+    entry = entry_of(g + kGroups);
+    const uint32_t scale_sel = 0x4040u | (static_cast<uint32_t>(v >> 1) * 0x0101u);  // byte v/2 to bytes 0 and 2
+    for (int j = g; j < nb; j += kGroups) {
+      const int s = j % kStages;
+      const int row_next = resolve(P, entry, k0 + (j + kGroups) * kBN + 32 * w + lane);
+      entry = entry_of(j + 2 * kGroups);
+      const uint8_t *src_l = P.cache + static_cast<int64_t>(row) * P.g.row_bytes;
+      const uint32_t factors = row >= 0 ? int4_row_factors(__ldg(src_l + P.g.exponent)) : 0u;
+      const uint32_t used = __ballot_sync(0xffffffffu, row >= 0);
+      // stages 1 and 2 held the staged Q until the softmax warps moved it to TMEM;
+      // the lanes shuffle below, so they go on or give up together
+      const bool go = mbar_wait(&kv_empty[s], ((j / kStages) & 1) ^ 1, P.err, 66, j) &&
+                      ((j != 1 && j != 2) || mbar_wait(q_ready, 0, P.err, 67, j));
+      if (!__all_sync(0xffffffffu, go)) break;
+      const uint32_t sb = smem_u32(smem + kOffStage + s * kStageBytes);
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {  // four rows of the lane in flight
+        uint32_t code[4][4], scales[4], fac[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int l = 16 * h + 4 * q + r4;  // the row within the warp's 32
+          const int rw = __shfl_sync(0xffffffffu, row, l);
+          fac[q] = __shfl_sync(0xffffffffu, factors, l);
+          const uint8_t *src = P.cache + static_cast<int64_t>(rw) * P.g.row_bytes;
+          code[q][0] = code[q][1] = code[q][2] = code[q][3] = scales[q] = 0u;
+          if (rw >= 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              code[q][i] = __ldg(reinterpret_cast<const uint32_t *>(src + main_dim0 / 2 + 32 * i + 4 * v));
+            scales[q] = __ldg(reinterpret_cast<const uint32_t *>(src + P.g.scales + main_dim0 / 16 + 4 * (v & 3)));
+          }
+          const int r = 32 * w + l;
+          if (v < 4)  // the rope columns: bf16 in the cache, four 16-byte units of the CTA's 32
+            cp_async_16(sb + kStageMain + r * 64 + ((v ^ ((r >> 1) & 3)) << 4),
+                        rw >= 0 ? src + P.g.rope + 64 * crank + 16 * v : P.cache, rw >= 0 ? 16u : 0u);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = 32 * w + 16 * h + 4 * q + r4;
+          const uint32_t f1 = __byte_perm(fac[q], 0, 0x1010), f2 = __byte_perm(fac[q], 0, 0x3232);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t word = __shfl_sync(0xffffffffu, scales[q], (lane & 24) + i);
+            const uint32_t sc = int4_scale(__byte_perm(word, 0, scale_sel), f1, f2);
+            uint32_t o[4];
+            int4_decode8(code[q][i], sc, int4_scale24(sc), o);
+            st_shared_v4(sb + i * (kBN * 128) + r * 128 + ((v ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+      if (lane == 0) masks[2 * s + w] = used;
+      cp_async_commit();
+      cp_async_wait<0>();
+      fence_proxy_async_smem();
+      mbar_arrive(&kv_full[s]);
+      row = row_next;
+    }
+    cp_async_wait<0>();
+  } else {
+    // ---------------- softmax: two warpgroups; thread = head row h = TMEM lane,
+    // warpgroup w owns columns [32w, 32w + 32) of every block.  Every decision
+    // that guards a tcgen05.ld/st (.sync.aligned) is made warp-uniform.
+    const int h = tid & 127, w = tid >> 7;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, P.err, 68, -1));
+    if (ok) {
+      // Q main dims: staged rows (128B swizzle) -> TMEM as bf16 pairs, chunks split by warpgroup
+      const uint8_t *qs = smem + kOffQStage;
+#pragma unroll 1
+      for (int i = w; i < kNMain; i += 2) {
+        uint32_t r[32];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(qs + i * 16384 + h * 128 + ((u ^ (h & 7)) << 4));
+          r[4 * u + 0] = x.x;
+          r[4 * u + 1] = x.y;
+          r[4 * u + 2] = x.z;
+          r[4 * u + 3] = x.w;
+        }
+        tmem_st32(lane_base + kQCol + 32 * i, r);
+      }
+      tmem_st_wait();
+    }
+    tc_fence_before();
+    warp_arrive(q_ready, lane);
+
+    uint8_t *recv0 = smem + kOffRecv;
+    // our 32 columns of a partial S row, rounded to fp16, for the exchange agent
+    auto stage = [&](int j, const float (&x)[32]) {
+      uint8_t *rowp = smem + kOffStg + (j & 1) * kRecvBytes + h * 128;
+#pragma unroll
+      for (int k = 0; k < 32; k += 8) {
+        const int u = (w * kHalf + k) >> 3;
+        *reinterpret_cast<uint4 *>(rowp + ((u ^ (h & 7)) << 4)) =
+            make_uint4(pack_f16x2_sat(x[k], x[k + 1]), pack_f16x2_sat(x[k + 2], x[k + 3]),
+                       pack_f16x2_sat(x[k + 4], x[k + 5]), pack_f16x2_sat(x[k + 6], x[k + 7]));
+      }
+      fence_proxy_async_smem();  // the bulk copy reads the tile through the async proxy
+      warp_arrive(&staged[j & 1], lane);
+    };
+    // our 32 columns of S(j), raw q.k; the buffer is then free for QK(j+2)
+    const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
+    auto load_s = [&](int j, float (&x)[32]) {
+      uint32_t r[32];
+      tmem_ld32(lane_base + kSCol + (j & 1) * kBN + w * kHalf, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(r[k]);
+      tc_fence_before();
+      warp_arrive(&s_free[j & 1], lane);
+    };
+
+    float m_used = -__builtin_huge_valf(), l = 0.f;  // m in log2 units; l over this warpgroup's columns
+    float s_a[32], s_b[32];
+    if (ok) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[0], 0, P.err, 69, 0));
+      if (ok) {
+        tc_fence_after();
+        load_s(0, s_a);
+        stage(0, s_a);
+      }
+    }
+    auto block = [&](int i, float (&x)[32], float (&nxt)[32]) -> bool {
+      const int b = i & 1;
+      if (i + 1 < nb) {
+        // fetch and ship block i+1 ahead: the peer has it by the time it starts block i+1
+        const int b1 = (i + 1) & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b1], ((i + 1) >> 1) & 1, P.err, 69, i + 1) &&
+                                         (i < 1 || mbar_wait(&stg_free[b1], ((i - 1) >> 1) & 1, P.err, 70, i + 1)));
+        if (!ok) return false;
+        tc_fence_after();
+        load_s(i + 1, nxt);
+        stage(i + 1, nxt);
+      }
+      if (tid == 0) mbar_arrive_expect_tx(&recv_full[b], kRecvBytes);
+      // the block's rows were complete before its QK; waiting on their barrier too orders the mask word read below
+      ok = __all_sync(0xffffffffu, mbar_wait<true>(&recv_full[b], (i >> 1) & 1, P.err, 71, i) &&
+                                       mbar_wait(&kv_full[i % kStages], (i / kStages) & 1, P.err, 71, i));
+      if (!ok) return false;
+      const uint8_t *my_recv = recv0 + b * kRecvBytes + h * 128;
+#pragma unroll
+      for (int k = 0; k < 32; k += 8) {
+        const int u = (w * kHalf + k) >> 3;
+        const uint4 t = *reinterpret_cast<const uint4 *>(my_recv + ((u ^ (h & 7)) << 4));
+        const uint32_t pv[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float lo, hi;
+          unpack_f16x2(pv[e], lo, hi);
+          f2_unpack(f2_add(f2_pack(x[k + 2 * e], x[k + 2 * e + 1]), f2_pack(lo, hi)), x[k + 2 * e], x[k + 2 * e + 1]);
+        }
+      }
+      const uint32_t used = masks[2 * (i % kStages) + w];
+      if (used != 0xffffffffu) {
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+          if (!((used >> k) & 1u)) x[k] = -__builtin_huge_valf();
+      }
+      float m3[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        m3[q] = fmax3(fmax3(x[8 * q], x[8 * q + 1], x[8 * q + 2]), fmax3(x[8 * q + 3], x[8 * q + 4], x[8 * q + 5]),
+                      fmaxf(x[8 * q + 6], x[8 * q + 7]));
+      red[(b * 2 + w) * 128 + h] = fmaxf(fmax3(m3[0], m3[1], m3[2]), m3[3]);
+      warp_arrive(&red_full[b], lane);
+      ok = __all_sync(0xffffffffu, mbar_wait(&red_full[b], (i >> 1) & 1, P.err, 72, i));
+      if (!ok) return false;
+      const float mblk = fmaxf(red[(b * 2) * 128 + h], red[(b * 2 + 1) * 128 + h]) * P.scale_log2;  // log2 units
+      // lazy rescale: only when some row of the warp saw its max grow by more
+      // than 2^8.  Both warpgroups see the same row maxima, so they decide alike.
+      if (__any_sync(0xffffffffu, mblk > m_used + 8.f)) {
+        const float m_new = fmaxf(m_used, mblk);
+        const float alpha = m_new > m_used ? ex2(m_used - m_new) : 1.f;  // both -inf: nothing yet
+        if (i >= 1) {
+          // O holds PV(i-1): rescale this warpgroup's half of it before PV(i) accumulates
+          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, P.err, 73, i));
+          if (!ok) return false;
+          tc_fence_after();
+          scale_o(lane_base, w * (kDvc / 2), (w + 1) * (kDvc / 2), alpha);
+          tc_fence_before();
+        }
+        l *= alpha;
+        m_used = m_new;
+      }
+      uint32_t packed[16];
+      // while no entry has been seen, m is -inf and every x too: any finite m gives e^x = 0
+      const float nm = m_used == -__builtin_huge_valf() ? 0.f : -m_used;
+      const uint64_t nm2 = f2_pack(nm, nm);
+      uint64_t acc[2] = {0, 0};  // +0.0f pairs
+#pragma unroll
+      for (int k = 0; k < 32; k += 2) {
+        float t0, t1;
+        f2_unpack(f2_fma(f2_pack(x[k], x[k + 1]), sc2, nm2), t0, t1);
+        const float e0 = ex2(t0), e1 = ex2(t1);
+        packed[k >> 1] = pack_bf16x2(e0, e1);
+        acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1], f2_pack(e0, e1));
+      }
+      float s0, s1, s2, s3;
+      f2_unpack(acc[0], s0, s1);
+      f2_unpack(acc[1], s2, s3);
+      l += (s0 + s1) + (s2 + s3);
+      uint8_t *prow = recv0 + b * kRecvBytes + h * 128;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int uu = w * 4 + u;
+        *reinterpret_cast<uint4 *>(prow + ((uu ^ (h & 7)) << 4)) =
+            make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&p_full[b], lane);
+      return true;
+    };
+    for (int i = 0; ok && i < nb; i += 2) {
+      ok = block(i, s_a, s_b);
+      if (ok && i + 1 < nb) ok = block(i + 1, s_b, s_a);
+    }
+    ok = __all_sync(0xffffffffu, ok && mbar_wait(&pv_done[(nb - 1) & 1], ((nb - 1) >> 1) & 1, P.err, 74, nb));
+    // the two warpgroups' partial sums of the softmax denominator
+    red[(4 + w) * 128 + h] = l;
+    warp_arrive(fin_full, lane);
+    ok = __all_sync(0xffffffffu, mbar_wait(fin_full, 0, P.err, 75) && ok);
+    l = red[4 * 128 + h] + red[5 * 128 + h];
+    tc_fence_after();
+    uint8_t *ost = smem + kOffStage;  // free: every PV is done
+    if (P.splits == 1) {
+      if (P.sink && h < P.H) l += ex2(P.sink[h] * 1.4426950408889634f - m_used);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // normalised rows through shared memory, 16-byte unit u of row h at
+      // u ^ (h & 31), so that neither the row-wise writes nor the reads
+      // collide; then each warp stores whole 512-byte rows
+      if (ok) {
+#pragma unroll 1
+        for (int c = w * (kDvc / 2); c < (w + 1) * (kDvc / 2); c += 32) {
+          uint32_t r[32];
+          tmem_ld32(lane_base + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            const int u = (c + k) >> 3;
+            *reinterpret_cast<uint4 *>(ost + h * 512 + ((u ^ (h & 31)) << 4)) =
+                make_uint4(pack_bf16x2(__uint_as_float(r[k + 0]) * inv, __uint_as_float(r[k + 1]) * inv),
+                           pack_bf16x2(__uint_as_float(r[k + 2]) * inv, __uint_as_float(r[k + 3]) * inv),
+                           pack_bf16x2(__uint_as_float(r[k + 4]) * inv, __uint_as_float(r[k + 5]) * inv),
+                           pack_bf16x2(__uint_as_float(r[k + 6]) * inv, __uint_as_float(r[k + 7]) * inv));
+          }
+        }
+      }
+      warp_arrive(o_staged, lane);
+      ok = __all_sync(0xffffffffu, mbar_wait(o_staged, 0, P.err, 76) && ok);
+      if (ok) {
+#pragma unroll 4
+        for (int hh = warp; hh < P.H; hh += 8) {
+          const uint4 x = *reinterpret_cast<const uint4 *>(ost + hh * 512 + ((lane ^ (hh & 31)) << 4));
+          *reinterpret_cast<uint4 *>(out_row + static_cast<int64_t>(hh) * kDv + lane * 8) = x;
+        }
+      }
+    } else {
+      // this split's part: O as it is (fp32), unit u of row h at u ^ (h & 63)
+      // in shared memory and in the workspace alike, one bulk copy of H KB
+      if (ok) {
+#pragma unroll 1
+        for (int c = w * (kDvc / 2); c < (w + 1) * (kDvc / 2); c += 32) {
+          uint32_t r[32];
+          tmem_ld32(lane_base + c, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            const int u = (c + k) >> 2;
+            *reinterpret_cast<uint4 *>(ost + h * 1024 + ((u ^ (h & 63)) << 4)) =
+                make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+          }
+        }
+        if (w == 0 && h < P.H) P.part_ml[half * P.H + h] = make_float2(m_used, l);
+      }
+      fence_proxy_async_smem();
+      warp_arrive(o_staged, lane);
+      if (tid == 0 && mbar_wait(o_staged, 0, P.err, 76) && ok) {
+        bulk_store(P.part_o + half * P.H * kDvc, ost, static_cast<uint32_t>(P.H) * kDvc * 4);
+        bulk_commit();
+        bulk_wait_read0();
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+  cluster_sync();  // no CTA leaves while its peer may still touch its smem
+}
+
+// Join the splits of one query and head: the parts' weights are e^(m_s - m)
+// with m their largest, the sum runs in split order.  One block per (query,
+// head), a thread on four value columns.
+__global__ void __launch_bounds__(128) sparse_attn_int4_join_kernel(const AttnInt4Params P) {
+  const int query = blockIdx.x, h = blockIdx.y;
+  int qrow = P.q_rows ? P.q_rows[query] : query;
+  if (qrow < 0 || qrow >= P.num_q_rows) return;  // the latter reported by the first kernel
+  const int crank = threadIdx.x >> 6, u = threadIdx.x & 63;
+  const int64_t first = static_cast<int64_t>(query) * P.splits * 2 + crank;
+  const float2 *ml = P.part_ml + first * P.H + h;
+  const float4 *o = reinterpret_cast<const float4 *>(P.part_o + (first * P.H + h) * kDvc) + (u ^ (h & 63));
+  const int64_t step = 2 * static_cast<int64_t>(P.H);  // rows of the same half between splits
+  float m = -__builtin_huge_valf();
+  for (int s = 0; s < P.splits; ++s) m = fmaxf(m, ml[s * step].x);
+  const float m0 = m == -__builtin_huge_valf() ? 0.f : m;
+  float l = P.sink ? ex2(P.sink[h] * 1.4426950408889634f - m) : 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  bool any = false;
+  for (int s = 0; s < P.splits; ++s) {
+    const float2 t = ml[s * step];
+    if (t.y == 0.f) continue;  // no entry: its O was not written
+    any = true;
+    const float wgt = ex2(t.x - m0);
+    const float4 x = o[s * step * (kDvc / 4)];
+    l += wgt * t.y;
+    acc.x += wgt * x.x;
+    acc.y += wgt * x.y;
+    acc.z += wgt * x.z;
+    acc.w += wgt * x.w;
+  }
+  const float inv = any && l != 0.f ? 1.f / l : 0.f;
+  uint2 r = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2 *>(P.out + (static_cast<int64_t>(qrow) * P.H + h) * kDv + crank * kDvc + 4 * u) = r;
+}
+
+// Entries per split.  A cluster's time is a fixed part (set-up, Q, the first
+// block's chain, the O half) plus one part per block of 64 entries; with s
+// splits there are n * s clusters for the device's SM pairs.
+int splits_for(int64_t n, int topk, int sms) {
+  const int blocks = (topk + kBN - 1) / kBN, pairs = sms / 2 > 0 ? sms / 2 : 1;
+  int best = 1;
+  double best_cost = 1e300;
+  for (int s = 1; s <= blocks && s <= 32; ++s) {
+    const int per = (blocks + s - 1) / s;
+    if ((blocks + per - 1) / per != s) continue;  // the same division as a smaller s
+    const double waves = static_cast<double>((n * s + pairs - 1) / pairs);
+    const double cost = waves * (5.0 + per) + (s > 1 ? 3.0 + 0.03 * static_cast<double>(n * s) : 0.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+}  // namespace
+}  // namespace dsa
+
+using namespace dsa;
+
+static size_t part_bytes(int64_t n, int splits, int H) {
+  return splits > 1 ? static_cast<size_t>(n) * splits * 2 * H * (kDvc * 4 + 8) : 0;
+}
+
+extern "C" dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t topk, size_t *bytes) {
+  if (!bytes) return DSA_ERR_INVALID_ARG;
+  if (n < 0 || topk < 1) return DSA_ERR_SHAPE;
+  if (H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
+  *bytes = n == 0 ? 0 : part_bytes(n, splits_for(n, topk, num_sms()), H);
+  return DSA_OK;
+}
+
+extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, const int32_t *q_rows, int32_t n,
+                                             const void *kv_cache, int32_t num_cache_rows, const int32_t *slots,
+                                             int32_t num_kv_rows, const int32_t *topk_idx, int32_t topk,
+                                             const float *attn_sink, float softmax_scale, int32_t H, int32_t D,
+                                             int32_t Dv, void *out, void *workspace, size_t ws_bytes,
+                                             dsa_stream_t stream) {
+  if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f) return DSA_ERR_INVALID_ARG;
+  if (n < 0 || num_q_rows < 0 || num_cache_rows < 0 || num_kv_rows < 0 || topk < 1) return DSA_ERR_SHAPE;
+  if (!q_rows && n > num_q_rows) return DSA_ERR_SHAPE;
+  if (D != kD || Dv != kDv || H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
+  if (n == 0 || num_q_rows == 0) return DSA_OK;
+  if (!q || !kv_cache || !topk_idx || !out) return DSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+  const int splits = splits_for(n, topk, num_sms());
+  const size_t need = part_bytes(n, splits, H);
+  if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return DSA_ERR_WORKSPACE;
+  if (static_cast<int64_t>(n) * splits * 2 > INT32_MAX) return DSA_ERR_SHAPE;
+  int *err = device_error_word();
+  if (!err) return DSA_ERR_CUDA;
+
+  AttnInt4Params P{};
+  P.cache = static_cast<const uint8_t *>(kv_cache);
+  P.slots = slots;
+  P.idx = topk_idx;
+  P.q_rows = q_rows;
+  P.sink = attn_sink;
+  P.out = static_cast<__nv_bfloat16 *>(out);
+  P.part_o = static_cast<float *>(workspace);
+  P.part_ml = reinterpret_cast<float2 *>(static_cast<float *>(workspace) +
+                                         static_cast<int64_t>(n) * splits * 2 * H * kDvc);
+  P.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
+  P.H = H;
+  P.topk = topk;
+  P.splits = splits;
+  const int blocks = (topk + kBN - 1) / kBN;
+  P.split_len = (blocks + splits - 1) / splits * kBN;
+  P.num_kv_rows = num_kv_rows;
+  P.cache_rows = num_cache_rows;
+  P.num_q_rows = num_q_rows;
+  dsa_status st = int4_geom(D, Dv, &P.g);
+  if (st != DSA_OK) return st;
+  P.err = err;
+
+  CUtensorMap qmain, qtail;
+  const uint64_t dims[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(H), static_cast<uint64_t>(num_q_rows)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(kD) * 2, static_cast<uint64_t>(H) * kD * 2};
+  const uint32_t box_main[3] = {64, kHeads, 1}, box_tail[3] = {32, kHeads, 1};
+  st = encode_tensor_map(&qmain, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box_main,
+                         CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != DSA_OK) return st;
+  st = encode_tensor_map(&qtail, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box_tail,
+                         CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != DSA_OK) return st;
+  cudaError_t e = cudaFuncSetAttribute(sparse_attn_int4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n) * splits * 2u);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_kernel, qmain, qtail, P);
+  if (e != cudaSuccess) return cuda_fail(e);
+  if (splits > 1)
+    sparse_attn_int4_join_kernel<<<dim3(static_cast<unsigned>(n), static_cast<unsigned>(H)), 128, 0, cfg.stream>>>(P);
+  return check_launch();
+}

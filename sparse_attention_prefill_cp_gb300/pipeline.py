@@ -26,6 +26,7 @@ from . import (HEAD_TAIL, IN_SEQ_SPLIT, ROUND_ROBIN, CPLocalMetadata, dsa_cp_all
                dsa_indexer_topk_workspace_size, dsa_kv_fp8_dequantize, dsa_kv_fp8_row_bytes, dsa_sparse_attn_prefill,
                dsa_sparse_attn_prefill_flat, dsa_sparse_attn_prefill_fp8kv, dsa_sparse_attn_prefill_headsharded,
                dsa_sparse_attn_prefill_swa,
+               dsa_kv_int4_dequantize, dsa_sparse_attn_int4kv, dsa_sparse_attn_int4kv_workspace_size,
                dsa_swa_index)
 
 
@@ -33,7 +34,8 @@ class DSAPrefill:
     def __init__(self, lengths, cp_size: int, mode: int, H: int, D: int, Dv: int, HI: int, DI: int, topk: int,
                  softmax_scale: float, device=None, workspace_bytes: int | None = None, view_streams: int = 1,
                  prefix_lens=None, kv_fp8: bool = False, fused: bool = False, compress_ratio: int = 1,
-                 index_fp8: bool = False, window: int = 0, kv_fp8_direct: bool = False):
+                 index_fp8: bool = False, window: int = 0, kv_fp8_direct: bool = False, kv_int4: bool = False,
+                 kv_int4_direct: bool = False):
         """``lengths``: query tokens per request.  ``prefix_lens`` (chunked
         prefill): KV positions per request that precede its queries; the KV
         and index-key tensors passed to ``run`` then hold every request's
@@ -42,7 +44,13 @@ class DSAPrefill:
         dsa_kv_fp8_row_bytes), dequantised once per batch before the views;
         with ``kv_fp8_direct`` the attention reads the cache itself and
         dequantises in its gather (dsa_sparse_attn_prefill_fp8kv, the same
-        results; DeepSeek-V3.2 shapes, no window).
+        results; DeepSeek-V3.2 shapes, no window).  ``kv_int4``: the latent
+        KV passed to ``run`` is the 4-bit cache (uint8 rows of
+        dsa_kv_int4_row_bytes; ``run``'s kv_slots int32 [num_kv_rows] gives
+        the cache row of every KV row where they are not in order),
+        dequantised once per batch, or with ``kv_int4_direct`` read by the
+        attention itself (dsa_sparse_attn_int4kv: no bf16 copy of the rows;
+        D 576, Dv 512, no window).
         ``fused``: ``run`` skips the split of q and the rerange of the
         outputs; each view's attention reads its queries from the full q and
         writes its rows of ``out`` in place (dsa_sparse_attn_prefill_flat),
@@ -104,8 +112,16 @@ class DSAPrefill:
         self.kv_fp8_direct = bool(kv_fp8_direct)
         if self.kv_fp8_direct and (not self.kv_fp8 or window):
             raise ValueError("kv_fp8_direct needs kv_fp8 and no window")
+        self.kv_int4 = bool(kv_int4)
+        self.kv_int4_direct = bool(kv_int4_direct)
+        if self.kv_int4 and self.kv_fp8:
+            raise ValueError("the latent KV is one cache: kv_fp8 or kv_int4")
+        if self.kv_int4_direct and (not self.kv_int4 or window or (D, Dv) != (576, 512)):
+            raise ValueError("kv_int4_direct needs kv_int4, no window, and D 576, Dv 512")
+        self._kv_slots = None
         self.kv_rows = (torch.empty((self.num_kv_rows, D), dtype=torch.bfloat16, device=dev)
-                        if self.kv_fp8 and not self.kv_fp8_direct else None)
+                        if (self.kv_fp8 and not self.kv_fp8_direct) or (self.kv_int4 and not self.kv_int4_direct)
+                        else None)
         self.attention_events = None  # a list: (view, start, end) CUDA events of every attention launch
         self._q = None
         self.window = int(window)
@@ -140,8 +156,9 @@ class DSAPrefill:
 
     def launches_per_step(self) -> int:
         """Kernel launches of one ``run``: metadata per view, 3 splits (2
-        fused), the FP8 dequantisation (if any), per view (indexer + top-k) per
-        workspace chunk and one attention, 1 rerange (0 fused)."""
+        fused), the cache's dequantisation (if any), per view (indexer + top-k)
+        per workspace chunk and one attention (two where the attention over the
+        4-bit cache is split), 1 rerange (0 fused)."""
         ld = (self.max_kv_len + 3) // 4 * 4
         tile = 8 if self.HI == 64 else 128
         rows_fit = (self.workspace.numel() // (ld * 4)) // tile * tile
@@ -149,8 +166,9 @@ class DSAPrefill:
         splits, reranges = (2, 0) if self.fused else (3, 1)
         md = self.cp_size * (2 if self.window and self.compress_ratio > 1 else 1)
         swa = self.cp_size if self.window else 0
-        dequant = int(self.kv_fp8 and not self.kv_fp8_direct)
-        return md + splits + dequant + self.cp_size * (2 * chunks + 1) + swa + reranges
+        dequant = int(self.kv_rows is not None)
+        joins = int(self.kv_int4_direct and dsa_sparse_attn_int4kv_workspace_size(self.tpr, self.H, self.topk) > 0)
+        return md + splits + dequant + self.cp_size * (2 * chunks + 1 + joins) + swa + reranges
 
     def metadata(self, stream=None):                                     # a1
         for r in range(self.cp_size):
@@ -192,6 +210,12 @@ class DSAPrefill:
             q, out = (self._q, self.out) if self.fused else (self.q_split[r], self.out_split[r])
             dsa_sparse_attn_prefill_fp8kv(self.md[r], q, kv, self.topk_idx[r], self.scale, self.D, self.Dv, out, sink,
                                           flat=self.fused, stream=st)
+        elif self.kv_int4_direct:
+            # a view's pad slots have no entries: zero rows in the view layout, no row in the flat one
+            flat = self.fused
+            dsa_sparse_attn_int4kv(self._q if flat else self.q_split[r], kv, self.topk_idx[r], self.scale, self.Dv,
+                                   sink, self._kv_slots, self.md[r].buffer[-self.tpr:] if flat else None,
+                                   self.out if flat else self.out_split[r], stream=st)
         elif self.fused:
             dsa_sparse_attn_prefill_flat(self.md[r], self._q, kv, self.topk_idx[r], self.scale, self.Dv, self.out,
                                          sink, st)
@@ -204,10 +228,13 @@ class DSAPrefill:
 
     def latent_kv(self, kv, stream=None):
         """The bf16 latent rows the attention reads: ``kv`` itself, or the
-        rows an FP8 cache stands for (dequantised into a buffer of this
-        object)."""
-        if not self.kv_fp8 or self.kv_fp8_direct:
+        rows a cache stands for (dequantised into a buffer of this object)."""
+        if self.kv_rows is None:
             return kv
+        if self.kv_int4:
+            if self._kv_slots is None and kv.shape[0] != self.num_kv_rows:
+                raise ValueError("without kv_slots the cache must hold the batch's KV rows in order")
+            return dsa_kv_int4_dequantize(kv, self.D, self.Dv, self._kv_slots, self.kv_rows, stream)
         return dsa_kv_fp8_dequantize(kv, self.D, self.Dv, self.kv_rows, stream)
 
     def side_streams(self):
@@ -241,12 +268,19 @@ class DSAPrefill:
             return self.out
         return dsa_cp_rerange(self.out_split, self.T, self.cp_size, self.mode, self.out, stream)
 
-    def run(self, q, kv, q_idx, k_idx, w, sink=None, stream=None, events=None, kv_ori=None):
+    def _take_slots(self, kv_slots):
+        if kv_slots is not None and (not self.kv_int4 or tuple(kv_slots.shape) != (self.num_kv_rows,)):
+            raise ValueError("kv_slots are the cache rows of every KV row of the batch (kv_int4)")
+        self._kv_slots = kv_slots
+
+    def run(self, q, kv, q_idx, k_idx, w, sink=None, stream=None, events=None, kv_ori=None, kv_slots=None):
         """One pass of the whole path; returns out [T, H, Dv] (a view of self.out).
         ``events``: optional dict of 4 CUDA events ("start", "core_start",
         "core_end", "end") recorded around the indexer/top-k/attention core.
         ``kv_ori``: the original latent rows for the sliding window at
-        compress_ratio > 1 (at ratio 1 the window reads ``kv``)."""
+        compress_ratio > 1 (at ratio 1 the window reads ``kv``).
+        ``kv_slots``: the cache row of every KV row (kv_int4)."""
+        self._take_slots(kv_slots)
         if self.window and self.compress_ratio > 1 and kv_ori is None:
             raise ValueError("the sliding window over compressed KV needs the original rows (kv_ori)")
         self._kv_ori = kv_ori if self.window and self.compress_ratio > 1 else None
@@ -281,11 +315,12 @@ class DSAPrefill:
         return dsa_cp_all_to_all_heads(self.out_split, self.T, self.cp_size, self.mode, self._head_sharded_buffer(),
                                        stream)
 
-    def run_headsharded(self, q, kv, q_idx, k_idx, w, sink=None, stream=None):
+    def run_headsharded(self, q, kv, q_idx, k_idx, w, sink=None, stream=None, kv_slots=None):
         """a1, a2, then per view a3 + a4 + a5 with the attention writing the
         head-sharded layout directly; returns out_hs [cp, T, H / cp, Dv]."""
-        if self.kv_fp8_direct:
-            raise ValueError("the head-sharded attention reads bf16 rows (build without kv_fp8_direct)")
+        if self.kv_fp8_direct or self.kv_int4_direct:
+            raise ValueError("the head-sharded attention reads bf16 rows (build without kv_fp8_direct / kv_int4_direct)")
+        self._take_slots(kv_slots)
         out = self._head_sharded_buffer()
         self.metadata(stream)
         self.split(q, q_idx, w, stream)

@@ -9,7 +9,9 @@ PyTorch only provides device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
+import functools
 
 import torch
 
@@ -38,6 +40,10 @@ def _stream(stream) -> C.c_void_p:
 
 def _ptr(t) -> C.c_void_p | None:
     return None if t is None else C.c_void_p(t.data_ptr())
+
+
+def _addr(t) -> int | None:
+    return None if t is None else t.data_ptr()
 
 
 def _need(t: torch.Tensor, dtype: torch.dtype, name: str) -> torch.Tensor:
@@ -596,45 +602,27 @@ def dsa_kv_fp8_dequantize(cache: torch.Tensor, D: int, Dv: int, out: torch.Tenso
     return out
 
 
-def _same_device(*tensors) -> torch.device:
-    """The one CUDA device of the given tensors (None skipped)."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if dev is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev} and {t.device}")
-        dev = t.device
-    return dev
+def _launch_on(stream, ref: torch.Tensor, **others):
+    """(context, stream handle) for a call whose tensors are ``ref`` and those
+    of ``others`` that are not None, all on one device.  The context makes
+    that device and ``stream`` (None: the device's current stream) current, so
+    that what the call allocates belongs to the stream its kernels run on; it
+    is None where they are already."""
+    dev = ref.device
+    for name, t in others.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
+    index = dev.index
+    handle = torch._C._cuda_getCurrentRawStream(index)
+    if stream is None:
+        return (None if index == torch.cuda.current_device() else torch.cuda.device(dev)), handle
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    same = stream.cuda_stream == handle and index == torch.cuda.current_device()
+    return (None if same else torch.cuda.stream(stream)), stream.cuda_stream
 
 
-class _launch_on:
-    """Make ``dev`` current and ``stream`` (or the device's current stream)
-    the current stream for the calls and allocations of the block: a tensor
-    allocated there belongs to the stream its kernel runs on."""
-
-    def __init__(self, dev: torch.device, stream):
-        self.ctx = []
-        if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-            if stream != torch.cuda.current_stream(dev) or dev.index != torch.cuda.current_device():
-                self.ctx.append(torch.cuda.stream(stream))
-        elif dev.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(dev))
-        self.dev = dev
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return C.c_void_p(torch.cuda.current_stream(self.dev).cuda_stream)
-
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
-        return False
-
-
+@functools.lru_cache(maxsize=None)
 def dsa_kv_int4_row_bytes(D: int, Dv: int) -> int:
     """Bytes of one 4-bit latent-KV cache row (include/dsa_cp.h)."""
     n = C.c_size_t()
@@ -667,11 +655,12 @@ def dsa_kv_int4_quantize(kv: torch.Tensor, Dv: int, out: torch.Tensor | None = N
         _need(out, torch.uint8, "out")
         if out.dim() != 2 or out.shape[1] != rb or (slots is None and out.shape[0] < n):
             raise ValueError(f"out must be [R, {rb}] with a row for every row written")
-    with _launch_on(_same_device(kv, out, slots), stream) as st:
+    ctx, st = _launch_on(stream, kv, out=out, slots=slots)
+    with ctx or contextlib.nullcontext():
         if out is None:
             out = torch.empty((n, rb), dtype=torch.uint8, device=kv.device)
-        check(load().dsa_kv_int4_quantize(_ptr(kv), stride, n, D, Dv, _ptr(slots), _ptr(out), out.shape[0], st),
-              "dsa_kv_int4_quantize")
+        check(load().dsa_kv_int4_quantize(kv.data_ptr(), stride, n, D, Dv, _addr(slots), out.data_ptr(), out.shape[0],
+                                          st), "dsa_kv_int4_quantize")
     return out
 
 
@@ -693,11 +682,12 @@ def dsa_kv_int4_dequantize(cache: torch.Tensor, D: int, Dv: int, rows: torch.Ten
         _need(out, torch.bfloat16, "out")
         if tuple(out.shape) != (n, D):
             raise ValueError(f"out must be [{n}, {D}]")
-    with _launch_on(_same_device(cache, rows, out), stream) as st:
+    ctx, st = _launch_on(stream, cache, rows=rows, out=out)
+    with ctx or contextlib.nullcontext():
         if out is None:
             out = torch.empty((n, D), dtype=torch.bfloat16, device=cache.device)
-        check(load().dsa_kv_int4_dequantize(_ptr(cache), cache.shape[0], D, Dv, _ptr(rows), n, _ptr(out), st),
-              "dsa_kv_int4_dequantize")
+        check(load().dsa_kv_int4_dequantize(cache.data_ptr(), cache.shape[0], D, Dv, _addr(rows), n, out.data_ptr(),
+                                            st), "dsa_kv_int4_dequantize")
     return out
 
 
@@ -753,17 +743,18 @@ def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: to
             raise ValueError(f"out must be [{m}, {H}, {Dv}]")
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
-    dev = _same_device(q, kv_cache, topk_idx, attn_sink, slots, q_rows, out, workspace)
-    with _launch_on(dev, stream) as st:
+    ctx, st = _launch_on(stream, q, kv_cache=kv_cache, topk_idx=topk_idx, attn_sink=attn_sink, slots=slots,
+                         q_rows=q_rows, out=out, workspace=workspace)
+    with ctx or contextlib.nullcontext():
         if out is None:
-            out = torch.empty((m, H, Dv), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((m, H, Dv), dtype=torch.bfloat16, device=q.device)
         if workspace is None:
             size = dsa_sparse_attn_int4kv_workspace_size(n, H, topk)
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-        check(load().dsa_sparse_attn_int4kv(_ptr(q), m, _ptr(q_rows), n, _ptr(kv_cache), kv_cache.shape[0],
-                                            _ptr(slots), 0 if slots is None else slots.shape[0], _ptr(topk_idx), topk,
-                                            _ptr(attn_sink), float(softmax_scale), H, D, Dv, _ptr(out),
-                                            _ptr(workspace), 0 if workspace is None else workspace.numel(), st),
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+        check(load().dsa_sparse_attn_int4kv(q.data_ptr(), m, _addr(q_rows), n, kv_cache.data_ptr(), kv_cache.shape[0],
+                                            _addr(slots), 0 if slots is None else slots.shape[0], topk_idx.data_ptr(),
+                                            topk, _addr(attn_sink), float(softmax_scale), H, D, Dv, out.data_ptr(),
+                                            _addr(workspace), 0 if workspace is None else workspace.numel(), st),
               "dsa_sparse_attn_int4kv")
     return out
 

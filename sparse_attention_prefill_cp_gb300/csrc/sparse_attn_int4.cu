@@ -20,16 +20,18 @@
 // are fp32.  A partial sum beyond 65504 saturates there.
 //
 // Tensor memory (512 columns): O (256), two S buffers (2 x 64), the CTA's 256
-// main Q dims as bf16 (128).  16 warps: 0-7 softmax in two warpgroups (one
+// main Q dims as bf16 (128).  14 warps: 0-7 softmax in two warpgroups (one
 // head row = one TMEM lane per thread; warpgroup w owns columns [32w, 32w + 32)
 // of every block of 64 entries), 8 TMA for Q then MMA issue, 9 the exchange
-// agent, 10-15 the gather: two warps per block, three blocks in flight.
+// agent, 10-13 the gather.  Nothing in the roles' loops is a call (a failed
+// wait or a bad index is noted and recorded at the end): a call's register
+// conventions made the softmax spill, and the gather's loads drove the spilled
+// values out of the small L1 that 227 KB of shared memory leave.
 //
 // The gather reads a row's codes, scales and exponent, decodes to bf16 with
 // one shift, one LOP3 and one packed fma per two values (no conversion
 // instructions: those share a pipe with the softmax's packing) and stores into
-// the swizzled tiles.  Index entries and slots are fetched two and one turns
-// ahead of the block that needs them.
+// the swizzled tiles.
 //
 // Splits: with few queries each query's entries are divided among several
 // clusters, which leave unnormalised fp32 O halves and (m, l) per head in the
@@ -48,7 +50,7 @@ constexpr int kHalf = kBN / 2;       // columns per softmax warpgroup
 constexpr int kStages = 4;
 constexpr int kNMain = 4;            // 64-wide latent chunks per CTA (128B swizzle), plus one of 32 (64B swizzle)
 constexpr int kDvc = 256;            // value columns per CTA
-constexpr int kThreads = 512;
+constexpr int kThreads = 448;
 constexpr int kQMain = kNMain * 128 * 128, kQTail = 128 * 64;
 constexpr int kStageMain = kNMain * kBN * 128, kStageBytes = kStageMain + kBN * 64;
 constexpr int kQKMainSteps = kNMain * 4, kQKSteps = kQKMainSteps + 2, kPVSteps = kBN / 16;
@@ -62,7 +64,7 @@ constexpr int kOffStg = kOffRecv + 2 * kRecvBytes;
 constexpr int kOffRed = kOffStg + 2 * kRecvBytes;     // [3][2 warpgroups][128] floats
 constexpr int kOffBar = kOffRed + 3 * 2 * 128 * 4;
 constexpr int kNumBars = 2 + 2 * kStages + 2 * 9 + 2;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;      // [0] tmem, [4..19] last used entry per warp, [20..27] masks
+constexpr int kOffMisc = kOffBar + kNumBars * 8;      // [0] tmem, [1] failed wait, [2..3] bad index, [4..19] last used entry per warp, [20..27] masks
 constexpr int kSmemBytes = kOffMisc + 28 * 4 + 1024;
 constexpr uint32_t kIdescQK = idesc_bf16(128, kBN, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16(128, kDvc, false, true);
@@ -99,9 +101,22 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// Multiply TMEM columns [c0, c1) of the warp's lanes by alpha.  Out of line:
-// it runs only when a row's max grows by more than 2^8.  Warp-collective.
-__device__ __noinline__ void scale_o(uint32_t lane_base, int c0, int c1, float alpha) {
+// mbar_wait without a call, for the loops that hold most of the registers:
+// bounded by the same time, the failing site and detail noted in shared memory.
+template <bool kCluster = false>
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int32_t *failed, int site, int detail = 0) {
+  if (kCluster ? mbar_try_wait_hint_cluster(bar, parity) : mbar_try_wait_hint(bar, parity)) return true;
+  const long long t0 = clock64();
+  do {
+    if (kCluster ? mbar_try_wait_hint_cluster(bar, parity) : mbar_try_wait_hint(bar, parity)) return true;
+  } while (clock64() - t0 < kWaitLimitCycles);
+  *failed = site << 24 | (detail & 0xffffff);
+  return false;
+}
+
+// Multiply TMEM columns [c0, c1) of the warp's lanes by alpha (it runs only
+// when a row's max grows by more than 2^8).  Warp-collective.
+__device__ __forceinline__ void scale_o(uint32_t lane_base, int c0, int c1, float alpha) {
 #pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
     uint32_t r[32];
@@ -114,23 +129,43 @@ __device__ __noinline__ void scale_o(uint32_t lane_base, int c0, int c1, float a
   tmem_st_wait();
 }
 
-// The cache row that an index entry names, -1 where it names none.
-__device__ __forceinline__ int resolve(const AttnInt4Params &P, int entry, int k) {
-  if (entry < 0) return -1;
-  int row = entry;
-  if (P.slots) {
-    if (entry >= P.num_kv_rows) {
-      record_error(P.err, DSA_ERR_DEVICE_BOUNDS, 49, k);
-      return -1;
-    }
-    row = __ldg(P.slots + entry);
-    if (row < 0) return -1;
+// The cache row that an index entry names (negative: none), unchecked: the
+// value of the slot load is not looked at before checked_row.
+__device__ __forceinline__ int slot_of(const AttnInt4Params &P, int32_t *bad, int entry, int k) {
+  if (!P.slots || entry < 0) return entry;
+  if (entry >= P.num_kv_rows) {
+    bad[0] = 49;
+    bad[1] = k;
+    return -1;
   }
+  return __ldg(P.slots + entry);
+}
+__device__ __forceinline__ int checked_row(const AttnInt4Params &P, int32_t *bad, int row, int k) {
   if (row >= P.cache_rows) {
-    record_error(P.err, DSA_ERR_DEVICE_BOUNDS, 50, k);
+    bad[0] = 50;
+    bad[1] = k;
     return -1;
   }
   return row;
+}
+
+// Loads of cache bytes, each used once on this SM; volatile, to be issued where they stand.
+__device__ __forceinline__ uint4 ld_once_v4(const void *p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_once_u16(const void *p) {
+  uint16_t r;
+  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_once_u8(const void *p) {
+  uint32_t r;
+  asm volatile("ld.global.nc.L1::no_allocate.u8 %0, [%1];" : "=r"(r) : "l"(p));
+  return r;
 }
 
 // The bulk copy of an O half out of shared memory.
@@ -147,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kOffBar);
   uint64_t *q_full = bars;                  // Q staged + tail landed (TMA)
   uint64_t *q_ready = bars + 1;             // Q main copied into TMEM, staging free (8 softmax warps)
-  uint64_t *kv_full = bars + 2;             // [kStages] rows decoded (64 gather threads)
+  uint64_t *kv_full = bars + 2;             // [kStages] rows decoded (4 gather warps)
   uint64_t *kv_empty = kv_full + kStages;   // [kStages] PV done with the stage (MMA commit)
   uint64_t *s_full = kv_empty + kStages;    // [2] QK done (MMA commit)
   uint64_t *s_free = s_full + 2;            // [2] S read out of TMEM (8 softmax warps)
@@ -162,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *o_staged = fin_full + 1;        // O rows staged in smem (8 warps)
   int32_t *misc = reinterpret_cast<int32_t *>(smem + kOffMisc);
   int32_t *last_used = misc + 4;
-  uint32_t *masks = reinterpret_cast<uint32_t *>(misc + 20);  // [kStages][2]: bit r of word w = row 32w + r is used
+  uint16_t *masks = reinterpret_cast<uint16_t *>(misc + 20);  // [kStages][4]: bit r of half-word w = row 16w + r is used
   float *red = reinterpret_cast<float *>(smem + kOffRed);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -194,9 +229,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (tid == 0) {
+    misc[1] = misc[2] = misc[3] = 0;
     mbar_init(q_ready, 8);
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&kv_full[s], 64);
+      mbar_init(&kv_full[s], 4);
       mbar_init(&kv_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -229,8 +265,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();
   tc_fence_after();
 #pragma unroll
-  for (int i = 0; i < 16; ++i) last = max(last, last_used[i]);
+  for (int i = 0; i < kThreads / 32; ++i) last = max(last, last_used[i]);
 
+  int32_t *failed = misc + 1;  // site and detail of a wait that gave up
+  int32_t *bad = misc + 2;     // site and position of an index that was out of range
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const int nb = (last + kBN - 1) / kBN;
   const int64_t half = static_cast<int64_t>(unit) * 2 + crank;  // of the workspace arrays
@@ -244,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(out_row + static_cast<int64_t>(u / (kDvc / 8)) * kDv + u % (kDvc / 8) * 8) =
             make_uint4(0u, 0u, 0u, 0u);
     }
-    if (q_issued) mbar_wait(q_full, 0, P.err, 60);  // the Q load issued at the start has landed
+    if (q_issued) wait_for(q_full, 0, failed, 60);  // the Q load issued at the start has landed
   } else if (warp == 8) {
     if (lane == 0) {
       // ---------------- MMA issuer, event-driven: QK(j) as soon as its rows are
@@ -257,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t pv_a0 = smem_desc(smem_u32(smem + kOffRecv), 16, 1024, kLayoutSW128);
       const uint64_t pv_b0 = smem_desc(st_addr, kBN * 128, 1024, kLayoutSW128);
       const uint32_t s_tm = tmem + kSCol, q_tm = tmem + kQCol;
-      bool ok = mbar_wait(q_full, 0, P.err, 61) && mbar_wait(q_ready, 0, P.err, 61);
+      bool ok = wait_for(q_full, 0, failed, 61) && wait_for(q_ready, 0, failed, 61);
       tc_fence_after();
       int qk = 0, pv = 0;
       long long t_prog = clock64(), t_check = t_prog;
@@ -301,10 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           t_prog = now;
         } else if (now - t_check > 100000) {
           t_check = now;
-          if (error_set(P.err)) {
-            ok = false;
-          } else if (now - t_prog > kWaitLimitCycles) {
-            record_error(P.err, DSA_ERR_DEVICE_TIMEOUT, 62, qk * 10000 + pv);
+          if (now - t_prog > kWaitLimitCycles) {
+            *failed = 62 << 24 | (pv & 0xffffff);
             ok = false;
           }
         }
@@ -320,8 +356,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; ok && t <= nb; ++t) {
         if (t < nb) {
           const int b = t & 1;
-          if (!(ok = mbar_wait(&staged[b], (t >> 1) & 1, P.err, 63, t))) break;
-          if (t >= 2 && !(ok = mbar_wait<true>(&recv_empty[b], ((t >> 1) & 1) ^ 1, P.err, 64, t))) break;
+          if (!(ok = wait_for(&staged[b], (t >> 1) & 1, failed, 63, t))) break;
+          if (t >= 2 && !(ok = wait_for<true>(&recv_empty[b], ((t >> 1) & 1) ^ 1, failed, 64, t))) break;
           bulk_copy_to_peer(peer_recv + b * kRecvBytes, smem + kOffStg + b * kRecvBytes, kRecvBytes, peer_full + b * 8);
           bulk_commit();
           bulk_wait_read0();
@@ -330,83 +366,96 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (t >= 1) {
           const int b = (t - 1) & 1;
           // PV(t-1) has read P(t-1), which sits in the tile the peer filled
-          if (!(ok = mbar_wait(&pv_done[b], ((t - 1) >> 1) & 1, P.err, 65, t - 1))) break;
+          if (!(ok = wait_for(&pv_done[b], ((t - 1) >> 1) & 1, failed, 65, t - 1))) break;
           mbar_arrive_remote_relaxed(&recv_empty[b], peer);
         }
       }
       bulk_wait_read0();
     }
   } else if (warp >= 10) {
-    // ---------------- gather: warps 10 + 2g and 11 + 2g take the blocks
-    // j = g (mod 3), warp w of them rows 32w .. 32w + 31.  Lane l knows row
-    // 32w + l of the block; to decode, eight lanes take one row, lane v of them
-    // unit v (8 columns) of each of the CTA's four 64-column chunks, so the
-    // stores of eight lanes fall on eight different bank groups.
-    constexpr int kGroups = 3;
-    const int g = (warp - 10) >> 1, w = (warp - 10) & 1;
-    const int v = lane & 7, r4 = lane >> 3;
+    // ---------------- gather: four warps, one on each sub-partition, so that
+    // none of the softmax warps shares its issue slots with more decoding than
+    // the others; warp w takes rows 16w .. 16w + 15 of every block.  Lane l
+    // knows row 16w + l % 16; to decode, eight lanes take one row, 32 columns
+    // each (one 16-byte load, two scales): lanes of one 8-lane store phase are
+    // two neighbours of four rows, and fall on eight different bank groups.
+    // A row's registers are loaded for the next block as soon as this block's
+    // row is decoded, so that a freed stage is full again after the decoding
+    // alone; slots are fetched one block before that, entries two.  An entry
+    // that names no row reads row 0 with factors of zero.
+    const int w = warp - 10, v = lane >> 2, r4 = lane & 3, own = 16 * w + (lane & 15);
     auto entry_of = [&](int j) {
-      const int k = j * kBN + 32 * w + lane;
+      const int k = j * kBN + own;
       return j < nb && k < last ? __ldg(idx_row + k0 + k) : -1;
     };
-    int entry = entry_of(g);
-    int row = resolve(P, entry, k0 + g * kBN + 32 * w + lane);
-    entry = entry_of(g + kGroups);
-    const uint32_t scale_sel = 0x4040u | (static_cast<uint32_t>(v >> 1) * 0x0101u);  // byte v/2 to bytes 0 and 2
-    for (int j = g; j < nb; j += kGroups) {
+    const uint8_t *const lane_codes = P.cache + main_dim0 / 2 + 16 * v;
+    const uint8_t *const lane_scales = P.cache + P.g.scales + main_dim0 / 16 + 2 * v;
+    uint4 code[4];
+    uint32_t scales[4], exponent;
+    auto load = [&](int q, int rr) {
+      const int64_t at = static_cast<int64_t>(__shfl_sync(0xffffffffu, rr, 4 * q + r4)) * P.g.row_bytes;
+      code[q] = ld_once_v4(lane_codes + at);
+      scales[q] = ld_once_u16(lane_scales + at);
+    };
+    int row = checked_row(P, bad, slot_of(P, bad, entry_of(0), k0 + own), k0 + own);
+    int row_next = slot_of(P, bad, entry_of(1), k0 + kBN + own), entry = entry_of(2);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) load(q, max(row, 0));
+    exponent = ld_once_u8(P.cache + static_cast<int64_t>(max(row, 0)) * P.g.row_bytes + P.g.exponent);
+    // the lane's place in a stage for row 4q + r4 and unit u of its four, less 512 q: place[(q & 1) * 4 + u]
+    uint32_t place[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      place[x] = (v >> 1) * (kBN * 128) + (16 * w + r4) * 128 + (((((v & 1) << 2) ^ r4) ^ x) << 4);
+#pragma unroll 1
+    for (int j = 0; j < nb; ++j) {
       const int s = j % kStages;
-      const int row_next = resolve(P, entry, k0 + (j + kGroups) * kBN + 32 * w + lane);
-      entry = entry_of(j + 2 * kGroups);
-      const uint8_t *src_l = P.cache + static_cast<int64_t>(row) * P.g.row_bytes;
-      const uint32_t factors = row >= 0 ? int4_row_factors(__ldg(src_l + P.g.exponent)) : 0u;
+      const uint32_t sb = smem_u32(smem + kOffStage + s * kStageBytes);
       const uint32_t used = __ballot_sync(0xffffffffu, row >= 0);
+      row_next = checked_row(P, bad, row_next, k0 + (j + 1) * kBN + own);
+      const int next0 = max(row_next, 0);
+      const int row_after = slot_of(P, bad, entry, k0 + (j + 2) * kBN + own);
+      entry = entry_of(j + 3);
       // stages 1 and 2 held the staged Q until the softmax warps moved it to TMEM;
       // the lanes shuffle below, so they go on or give up together
-      const bool go = mbar_wait(&kv_empty[s], ((j / kStages) & 1) ^ 1, P.err, 66, j) &&
-                      ((j != 1 && j != 2) || mbar_wait(q_ready, 0, P.err, 67, j));
+      const bool go = wait_for(&kv_empty[s], ((j / kStages) & 1) ^ 1, failed, 66, j) &&
+                      ((j != 1 && j != 2) || wait_for(q_ready, 0, failed, 67, j));
       if (!__all_sync(0xffffffffu, go)) break;
-      const uint32_t sb = smem_u32(smem + kOffStage + s * kStageBytes);
-#pragma unroll 1
-      for (int h = 0; h < 2; ++h) {  // four rows of the lane in flight
-        uint32_t code[4][4], scales[4], fac[4];
+      if (lane == 0) masks[4 * s + w] = static_cast<uint16_t>(used);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int l = 16 * h + 4 * q + r4;  // the row within the warp's 32
-          const int rw = __shfl_sync(0xffffffffu, row, l);
-          fac[q] = __shfl_sync(0xffffffffu, factors, l);
-          const uint8_t *src = P.cache + static_cast<int64_t>(rw) * P.g.row_bytes;
-          code[q][0] = code[q][1] = code[q][2] = code[q][3] = scales[q] = 0u;
-          if (rw >= 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              code[q][i] = __ldg(reinterpret_cast<const uint32_t *>(src + main_dim0 / 2 + 32 * i + 4 * v));
-            scales[q] = __ldg(reinterpret_cast<const uint32_t *>(src + P.g.scales + main_dim0 / 16 + 4 * (v & 3)));
-          }
-          const int r = 32 * w + l;
-          if (v < 4)  // the rope columns: bf16 in the cache, four 16-byte units of the CTA's 32
-            cp_async_16(sb + kStageMain + r * 64 + ((v ^ ((r >> 1) & 3)) << 4),
-                        rw >= 0 ? src + P.g.rope + 64 * crank + 16 * v : P.cache, rw >= 0 ? 16u : 0u);
-        }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int r = 32 * w + 16 * h + 4 * q + r4;
-          const uint32_t f1 = __byte_perm(fac[q], 0, 0x1010), f2 = __byte_perm(fac[q], 0, 0x3232);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t word = __shfl_sync(0xffffffffu, scales[q], (lane & 24) + i);
-            const uint32_t sc = int4_scale(__byte_perm(word, 0, scale_sel), f1, f2);
-            uint32_t o[4];
-            int4_decode8(code[q][i], sc, int4_scale24(sc), o);
-            st_shared_v4(sb + i * (kBN * 128) + r * 128 + ((v ^ (r & 7)) << 4), o[0], o[1], o[2], o[3]);
-          }
-        }
+      for (int x = 0; x < 2; ++x) {  // the rope columns: bf16 in the cache, four 16-byte units a row for this CTA
+        const int rl = 8 * x + (lane >> 2), r = 16 * w + rl, u = lane & 3;
+        const int rw = __shfl_sync(0xffffffffu, row, rl);
+        cp_async_16(sb + kStageMain + r * 64 + ((u ^ ((r >> 1) & 3)) << 4),
+                    P.cache + static_cast<int64_t>(max(rw, 0)) * P.g.row_bytes + P.g.rope + 64 * crank + 16 * u,
+                    rw >= 0 ? 16u : 0u);
       }
-      if (lane == 0) masks[2 * s + w] = used;
       cp_async_commit();
+      const uint32_t factors = row >= 0 ? int4_row_factors(exponent) : 0u;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t fac = __shfl_sync(0xffffffffu, factors, 4 * q + r4);
+        const uint32_t f1 = __byte_perm(fac, 0, 0x1010), f2 = __byte_perm(fac, 0, 0x3232);
+        const uint32_t words[4] = {code[q].x, code[q].y, code[q].z, code[q].w};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t sc = int4_scale(__byte_perm(scales[q], 0, b == 0 ? 0x4040 : 0x4141), f1, f2);
+          const uint32_t sc24 = int4_scale24(sc);
+#pragma unroll
+          for (int u = 2 * b; u < 2 * b + 2; ++u) {
+            uint32_t o[4];
+            int4_decode8(words[u], sc, sc24, o);
+            st_shared_v4(sb + place[(q & 1) * 4 + u] + 512 * q, o[0], o[1], o[2], o[3]);
+          }
+        }
+        load(q, next0);
+      }
+      exponent = ld_once_u8(P.cache + static_cast<int64_t>(next0) * P.g.row_bytes + P.g.exponent);
       cp_async_wait<0>();
       fence_proxy_async_smem();
-      mbar_arrive(&kv_full[s]);
+      warp_arrive(&kv_full[s], lane);
       row = row_next;
+      row_next = row_after;
     }
     cp_async_wait<0>();
   } else {
@@ -415,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // that guards a tcgen05.ld/st (.sync.aligned) is made warp-uniform.
     const int h = tid & 127, w = tid >> 7;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    bool ok = __all_sync(0xffffffffu, mbar_wait(q_full, 0, P.err, 68, -1));
+    bool ok = __all_sync(0xffffffffu, wait_for(q_full, 0, failed, 68, -1));
     if (ok) {
       // Q main dims: staged rows (128B swizzle) -> TMEM as bf16 pairs, chunks split by warpgroup
       const uint8_t *qs = smem + kOffQStage;
@@ -466,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m_used = -__builtin_huge_valf(), l = 0.f;  // m in log2 units; l over this warpgroup's columns
     float s_a[32], s_b[32];
     if (ok) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[0], 0, P.err, 69, 0));
+      ok = __all_sync(0xffffffffu, wait_for(&s_full[0], 0, failed, 69, 0));
       if (ok) {
         tc_fence_after();
         load_s(0, s_a);
@@ -478,8 +527,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i + 1 < nb) {
         // fetch and ship block i+1 ahead: the peer has it by the time it starts block i+1
         const int b1 = (i + 1) & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[b1], ((i + 1) >> 1) & 1, P.err, 69, i + 1) &&
-                                         (i < 1 || mbar_wait(&stg_free[b1], ((i - 1) >> 1) & 1, P.err, 70, i + 1)));
+        ok = __all_sync(0xffffffffu, wait_for(&s_full[b1], ((i + 1) >> 1) & 1, failed, 69, i + 1) &&
+                                         (i < 1 || wait_for(&stg_free[b1], ((i - 1) >> 1) & 1, failed, 70, i + 1)));
         if (!ok) return false;
         tc_fence_after();
         load_s(i + 1, nxt);
@@ -487,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (tid == 0) mbar_arrive_expect_tx(&recv_full[b], kRecvBytes);
       // the block's rows were complete before its QK; waiting on their barrier too orders the mask word read below
-      ok = __all_sync(0xffffffffu, mbar_wait<true>(&recv_full[b], (i >> 1) & 1, P.err, 71, i) &&
-                                       mbar_wait(&kv_full[i % kStages], (i / kStages) & 1, P.err, 71, i));
+      ok = __all_sync(0xffffffffu, wait_for<true>(&recv_full[b], (i >> 1) & 1, failed, 71, i) &&
+                                       wait_for(&kv_full[i % kStages], (i / kStages) & 1, failed, 71, i));
       if (!ok) return false;
       const uint8_t *my_recv = recv0 + b * kRecvBytes + h * 128;
 #pragma unroll
@@ -503,7 +552,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           f2_unpack(f2_add(f2_pack(x[k + 2 * e], x[k + 2 * e + 1]), f2_pack(lo, hi)), x[k + 2 * e], x[k + 2 * e + 1]);
         }
       }
-      const uint32_t used = masks[2 * (i % kStages) + w];
+      const uint32_t used = reinterpret_cast<const uint32_t *>(masks)[2 * (i % kStages) + w];
       if (used != 0xffffffffu) {
 #pragma unroll
         for (int k = 0; k < 32; ++k)
@@ -516,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                       fmaxf(x[8 * q + 6], x[8 * q + 7]));
       red[(b * 2 + w) * 128 + h] = fmaxf(fmax3(m3[0], m3[1], m3[2]), m3[3]);
       warp_arrive(&red_full[b], lane);
-      ok = __all_sync(0xffffffffu, mbar_wait(&red_full[b], (i >> 1) & 1, P.err, 72, i));
+      ok = __all_sync(0xffffffffu, wait_for(&red_full[b], (i >> 1) & 1, failed, 72, i));
       if (!ok) return false;
       const float mblk = fmaxf(red[(b * 2) * 128 + h], red[(b * 2 + 1) * 128 + h]) * P.scale_log2;  // log2 units
       // lazy rescale: only when some row of the warp saw its max grow by more
@@ -526,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = m_new > m_used ? ex2(m_used - m_new) : 1.f;  // both -inf: nothing yet
         if (i >= 1) {
           // O holds PV(i-1): rescale this warpgroup's half of it before PV(i) accumulates
-          ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, P.err, 73, i));
+          ok = __all_sync(0xffffffffu, wait_for(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, failed, 73, i));
           if (!ok) return false;
           tc_fence_after();
           scale_o(lane_base, w * (kDvc / 2), (w + 1) * (kDvc / 2), alpha);
@@ -567,11 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = block(i, s_a, s_b);
       if (ok && i + 1 < nb) ok = block(i + 1, s_b, s_a);
     }
-    ok = __all_sync(0xffffffffu, ok && mbar_wait(&pv_done[(nb - 1) & 1], ((nb - 1) >> 1) & 1, P.err, 74, nb));
+    ok = __all_sync(0xffffffffu, ok && wait_for(&pv_done[(nb - 1) & 1], ((nb - 1) >> 1) & 1, failed, 74, nb));
     // the two warpgroups' partial sums of the softmax denominator
     red[(4 + w) * 128 + h] = l;
     warp_arrive(fin_full, lane);
-    ok = __all_sync(0xffffffffu, mbar_wait(fin_full, 0, P.err, 75) && ok);
+    ok = __all_sync(0xffffffffu, wait_for(fin_full, 0, failed, 75) && ok);
     l = red[4 * 128 + h] + red[5 * 128 + h];
     tc_fence_after();
     uint8_t *ost = smem + kOffStage;  // free: every PV is done
@@ -599,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       warp_arrive(o_staged, lane);
-      ok = __all_sync(0xffffffffu, mbar_wait(o_staged, 0, P.err, 76) && ok);
+      ok = __all_sync(0xffffffffu, wait_for(o_staged, 0, failed, 76) && ok);
       if (ok) {
 #pragma unroll 4
         for (int hh = warp; hh < P.H; hh += 8) {
@@ -627,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       fence_proxy_async_smem();
       warp_arrive(o_staged, lane);
-      if (tid == 0 && mbar_wait(o_staged, 0, P.err, 76) && ok) {
+      if (tid == 0 && wait_for(o_staged, 0, failed, 76) && ok) {
         bulk_store(P.part_o + half * P.H * kDvc, ost, static_cast<uint32_t>(P.H) * kDvc * 4);
         bulk_commit();
         bulk_wait_read0();
@@ -636,6 +685,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *failed) record_error(P.err, DSA_ERR_DEVICE_TIMEOUT, *failed >> 24, *failed & 0xffffff);
+  if (tid == 0 && bad[0]) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, bad[0], bad[1]);
   if (warp == 8) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmemCols);
@@ -645,35 +696,46 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Join the splits of one query and head: the parts' weights are e^(m_s - m)
 // with m their largest, the sum runs in split order.  One block per (query,
-// head), a thread on four value columns.
+// head), a thread on four value columns, eight parts' loads in flight; the
+// weights come from one pass of the warps' lanes over the parts' (m, l).
+constexpr int kMaxSplits = 32;
 __global__ void __launch_bounds__(128) sparse_attn_int4_join_kernel(const AttnInt4Params P) {
-  const int query = blockIdx.x, h = blockIdx.y;
-  int qrow = P.q_rows ? P.q_rows[query] : query;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel may still run
+  const int query = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
+  const int qrow = P.q_rows ? P.q_rows[query] : query;
   if (qrow < 0 || qrow >= P.num_q_rows) return;  // the latter reported by the first kernel
   const int crank = threadIdx.x >> 6, u = threadIdx.x & 63;
   const int64_t first = static_cast<int64_t>(query) * P.splits * 2 + crank;
-  const float2 *ml = P.part_ml + first * P.H + h;
-  const float4 *o = reinterpret_cast<const float4 *>(P.part_o + (first * P.H + h) * kDvc) + (u ^ (h & 63));
   const int64_t step = 2 * static_cast<int64_t>(P.H);  // rows of the same half between splits
-  float m = -__builtin_huge_valf();
-  for (int s = 0; s < P.splits; ++s) m = fmaxf(m, ml[s * step].x);
-  const float m0 = m == -__builtin_huge_valf() ? 0.f : m;
+  float2 t = make_float2(-__builtin_huge_valf(), 0.f);
+  if (lane < P.splits) t = P.part_ml[first * P.H + h + lane * step];
+  float m = t.x;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  const unsigned parts = __ballot_sync(0xffffffffu, t.y != 0.f);  // the others have no entry, and no O was written
+  const float wgt = t.y != 0.f ? ex2(t.x - (m == -__builtin_huge_valf() ? 0.f : m)) : 0.f;
   float l = P.sink ? ex2(P.sink[h] * 1.4426950408889634f - m) : 0.f;
+  const float wl = t.y != 0.f ? wgt * t.y : 0.f;
+  const float4 *o = reinterpret_cast<const float4 *>(P.part_o + (first * P.H + h) * kDvc) + (u ^ (h & 63));
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  bool any = false;
-  for (int s = 0; s < P.splits; ++s) {
-    const float2 t = ml[s * step];
-    if (t.y == 0.f) continue;  // no entry: its O was not written
-    any = true;
-    const float wgt = ex2(t.x - m0);
-    const float4 x = o[s * step * (kDvc / 4)];
-    l += wgt * t.y;
-    acc.x += wgt * x.x;
-    acc.y += wgt * x.y;
-    acc.z += wgt * x.z;
-    acc.w += wgt * x.w;
+  for (int s0 = 0; s0 < P.splits; s0 += 8) {
+    float4 x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if ((parts >> (s0 + k)) & 1u) x[k] = o[(s0 + k) * step * (kDvc / 4)];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float w = __shfl_sync(0xffffffffu, wgt, s0 + k);
+      l += __shfl_sync(0xffffffffu, wl, s0 + k);
+      acc.x += w * x[k].x;
+      acc.y += w * x[k].y;
+      acc.z += w * x[k].z;
+      acc.w += w * x[k].w;
+    }
   }
-  const float inv = any && l != 0.f ? 1.f / l : 0.f;
+  const float inv = parts && l != 0.f ? 1.f / l : 0.f;
   uint2 r = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
   *reinterpret_cast<uint2 *>(P.out + (static_cast<int64_t>(qrow) * P.H + h) * kDv + crank * kDvc + 4 * u) = r;
 }
@@ -685,7 +747,7 @@ int splits_for(int64_t n, int topk, int sms) {
   const int blocks = (topk + kBN - 1) / kBN, pairs = sms / 2 > 0 ? sms / 2 : 1;
   int best = 1;
   double best_cost = 1e300;
-  for (int s = 1; s <= blocks && s <= 32; ++s) {
+  for (int s = 1; s <= blocks && s <= kMaxSplits; ++s) {
     const int per = (blocks + s - 1) / s;
     if ((blocks + per - 1) / per != s) continue;  // the same division as a smaller s
     const double waves = static_cast<double>((n * s + pairs - 1) / pairs);
@@ -722,7 +784,7 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
                                              int32_t Dv, void *out, void *workspace, size_t ws_bytes,
                                              dsa_stream_t stream) {
   if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f) return DSA_ERR_INVALID_ARG;
-  if (n < 0 || num_q_rows < 0 || num_cache_rows < 0 || num_kv_rows < 0 || topk < 1) return DSA_ERR_SHAPE;
+  if (n < 0 || num_q_rows < 0 || num_cache_rows < 1 || num_kv_rows < 0 || topk < 1) return DSA_ERR_SHAPE;
   if (!q_rows && n > num_q_rows) return DSA_ERR_SHAPE;
   if (D != kD || Dv != kDv || H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
   if (n == 0 || num_q_rows == 0) return DSA_OK;
@@ -784,7 +846,14 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_kernel, qmain, qtail, P);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (splits > 1)
-    sparse_attn_int4_join_kernel<<<dim3(static_cast<unsigned>(n), static_cast<unsigned>(H)), 128, 0, cfg.stream>>>(P);
+  if (splits > 1) {
+    cfg.gridDim = dim3(static_cast<unsigned>(n), static_cast<unsigned>(H));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_join_kernel, P);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
   return check_launch();
 }

@@ -9,7 +9,6 @@ PyTorch only provides device memory and streams.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import functools
 
@@ -602,24 +601,23 @@ def dsa_kv_fp8_dequantize(cache: torch.Tensor, D: int, Dv: int, out: torch.Tenso
     return out
 
 
-def _launch_on(stream, ref: torch.Tensor, **others):
+def _launch_on(stream, ref: torch.Tensor, *others):
     """(context, stream handle) for a call whose tensors are ``ref`` and those
     of ``others`` that are not None, all on one device.  The context makes
     that device and ``stream`` (None: the device's current stream) current, so
     that what the call allocates belongs to the stream its kernels run on; it
     is None where they are already."""
-    dev = ref.device
-    for name, t in others.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the other tensors on {dev}")
-    index = dev.index
+    index = ref.get_device()
+    for t in others:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"tensors on different devices: {ref.device} and {t.device}")
     handle = torch._C._cuda_getCurrentRawStream(index)
+    here = index == torch._C._cuda_getDevice()
     if stream is None:
-        return (None if index == torch.cuda.current_device() else torch.cuda.device(dev)), handle
-    if stream.device != dev:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    same = stream.cuda_stream == handle and index == torch.cuda.current_device()
-    return (None if same else torch.cuda.stream(stream)), stream.cuda_stream
+        return (None if here else torch.cuda.device(index)), handle
+    if stream.device != ref.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {ref.device}")
+    return (None if here and stream.cuda_stream == handle else torch.cuda.stream(stream)), stream.cuda_stream
 
 
 @functools.lru_cache(maxsize=None)
@@ -655,12 +653,17 @@ def dsa_kv_int4_quantize(kv: torch.Tensor, Dv: int, out: torch.Tensor | None = N
         _need(out, torch.uint8, "out")
         if out.dim() != 2 or out.shape[1] != rb or (slots is None and out.shape[0] < n):
             raise ValueError(f"out must be [R, {rb}] with a row for every row written")
-    ctx, st = _launch_on(stream, kv, out=out, slots=slots)
-    with ctx or contextlib.nullcontext():
+    ctx, st = _launch_on(stream, kv, out, slots)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if out is None:
             out = torch.empty((n, rb), dtype=torch.uint8, device=kv.device)
         check(load().dsa_kv_int4_quantize(kv.data_ptr(), stride, n, D, Dv, _addr(slots), out.data_ptr(), out.shape[0],
                                           st), "dsa_kv_int4_quantize")
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     return out
 
 
@@ -672,7 +675,7 @@ def dsa_kv_int4_dequantize(cache: torch.Tensor, D: int, Dv: int, rows: torch.Ten
     _need(cache, torch.uint8, "cache")
     if cache.dim() != 2 or cache.shape[1] != dsa_kv_int4_row_bytes(D, Dv):
         raise ValueError("cache rows do not have the 4-bit row size of (D, Dv)")
-    n = cache.shape[0]
+    n = R = cache.shape[0]
     if rows is not None:
         _need(rows, torch.int32, "rows")
         if rows.dim() != 1:
@@ -682,12 +685,17 @@ def dsa_kv_int4_dequantize(cache: torch.Tensor, D: int, Dv: int, rows: torch.Ten
         _need(out, torch.bfloat16, "out")
         if tuple(out.shape) != (n, D):
             raise ValueError(f"out must be [{n}, {D}]")
-    ctx, st = _launch_on(stream, cache, rows=rows, out=out)
-    with ctx or contextlib.nullcontext():
+    ctx, st = _launch_on(stream, cache, rows, out)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if out is None:
             out = torch.empty((n, D), dtype=torch.bfloat16, device=cache.device)
-        check(load().dsa_kv_int4_dequantize(cache.data_ptr(), cache.shape[0], D, Dv, _addr(rows), n, out.data_ptr(),
-                                            st), "dsa_kv_int4_dequantize")
+        check(load().dsa_kv_int4_dequantize(cache.data_ptr(), R, D, Dv, _addr(rows), n, out.data_ptr(), st),
+              "dsa_kv_int4_dequantize")
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     return out
 
 
@@ -696,6 +704,11 @@ def dsa_sparse_attn_int4kv_workspace_size(n: int, H: int, topk: int) -> int:
     b = C.c_size_t()
     check(load().dsa_sparse_attn_int4kv_workspace_size(n, H, topk, C.byref(b)), "dsa_sparse_attn_int4kv_workspace_size")
     return b.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _int4kv_workspace(device: int, n: int, H: int, topk: int) -> int:
+    return dsa_sparse_attn_int4kv_workspace_size(n, H, topk)  # with that device current
 
 
 def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: torch.Tensor, softmax_scale: float,
@@ -743,19 +756,24 @@ def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: to
             raise ValueError(f"out must be [{m}, {H}, {Dv}]")
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
-    ctx, st = _launch_on(stream, q, kv_cache=kv_cache, topk_idx=topk_idx, attn_sink=attn_sink, slots=slots,
-                         q_rows=q_rows, out=out, workspace=workspace)
-    with ctx or contextlib.nullcontext():
+    ctx, st = _launch_on(stream, q, kv_cache, topk_idx, attn_sink, slots, q_rows, out, workspace)
+    if ctx is not None:
+        ctx.__enter__()
+    try:
         if out is None:
             out = torch.empty((m, H, Dv), dtype=torch.bfloat16, device=q.device)
         if workspace is None:
-            size = dsa_sparse_attn_int4kv_workspace_size(n, H, topk)
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+            ws_bytes = _int4kv_workspace(q.get_device(), n, H, topk)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device) if ws_bytes else None
+        else:
+            ws_bytes = workspace.numel()
         check(load().dsa_sparse_attn_int4kv(q.data_ptr(), m, _addr(q_rows), n, kv_cache.data_ptr(), kv_cache.shape[0],
                                             _addr(slots), 0 if slots is None else slots.shape[0], topk_idx.data_ptr(),
                                             topk, _addr(attn_sink), float(softmax_scale), H, D, Dv, out.data_ptr(),
-                                            _addr(workspace), 0 if workspace is None else workspace.numel(), st),
-              "dsa_sparse_attn_int4kv")
+                                            _addr(workspace), ws_bytes, st), "dsa_sparse_attn_int4kv")
+    finally:
+        if ctx is not None:
+            ctx.__exit__(None, None, None)
     return out
 
 

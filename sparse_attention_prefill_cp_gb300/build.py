@@ -26,7 +26,8 @@ NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 
 # Per-source ptxas settings, measured: the attention kernel's pipelined loop
 # runs ~1 % faster with ptxas -O1 than with the default -O3 (same registers).
-SOURCE_FLAGS = {"sparse_attn.cu": ["-Xptxas", "-O1"], "sparse_attn_int4.cu": ["-Xptxas", "-O1"]}
+SOURCE_FLAGS = {"sparse_attn.cu": ["-Xptxas", "-O1"], "sparse_attn_int4.cu": ["-Xptxas", "-O1"],
+                "sparse_attn_int4_few.cu": ["-Xptxas", "-O1"]}
 
 
 def nvcc() -> str:

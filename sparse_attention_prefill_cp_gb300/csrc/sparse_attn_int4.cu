@@ -37,14 +37,14 @@
 // clusters, which leave unnormalised fp32 O halves and (m, l) per head in the
 // workspace; a second kernel joins them in split order (no atomics, so the
 // result does not depend on timing).
-#include "int4_common.cuh"
+#include "sparse_attn_int4.cuh"
 #include "internal.h"
 
 namespace dsa {
 namespace {
 
-constexpr int kD = 576, kDv = 512;
-constexpr int kHeads = 128;          // M of the MMAs
+constexpr int kD = kInt4D, kDv = kInt4Dv;
+constexpr int kHeads = kInt4MaxHeads;          // M of the MMAs
 constexpr int kBN = 64;              // entries per block
 constexpr int kHalf = kBN / 2;       // columns per softmax warpgroup
 constexpr int kStages = 4;
@@ -71,47 +71,13 @@ constexpr uint32_t kIdescPV = idesc_bf16(128, kDvc, false, true);
 static_assert(kQCol + kNMain * 32 <= kTmemCols, "TMEM budget");
 static_assert(kQMain <= 2 * kStageBytes, "Q staging fits in stages 1..2");
 static_assert(kStageBytes % 1024 == 0 && kOffQTail % 1024 == 0 && kOffRecv % 1024 == 0, "alignment");
-static_assert(kHeads * kDvc * 4 <= kStages * kStageBytes, "the fp32 O half fits in the stages");
+constexpr int kPartRow = kDvc * 4 + 16;
+static_assert(kHeads * kPartRow <= kStages * kStageBytes, "the fp32 O half fits in the stages");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
-
-struct AttnInt4Params {
-  const uint8_t *cache;    // [cache_rows][row_bytes]
-  const int32_t *slots;    // [num_kv_rows] KV row -> cache row (negative: no row), or nullptr: entries are cache rows
-  const int32_t *idx;      // [n][topk]
-  const int32_t *q_rows;   // [n] row of q and out (negative: none), or nullptr: row i
-  const float *sink;       // [H] or nullptr
-  __nv_bfloat16 *out;      // [num_q_rows][H][Dv]
-  float *part_o;           // [n * splits][2][H][256], 16-byte units swizzled (splits > 1)
-  float2 *part_ml;         // [n * splits][2][H] (splits > 1)
-  float scale_log2;        // softmax_scale * log2(e)
-  int32_t H, topk, splits, split_len;  // split_len: entries per split, a multiple of kBN
-  int32_t num_kv_rows, cache_rows, num_q_rows;
-  Int4Geom g;
-  int *err;
-};
 
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// mbar_wait without a call, for the loops that hold most of the registers:
-// bounded by the same time, the failing site and detail noted in shared memory.
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int32_t *failed, int site, int detail = 0) {
-  if (kCluster ? mbar_try_wait_hint_cluster(bar, parity) : mbar_try_wait_hint(bar, parity)) return true;
-  const long long t0 = clock64();
-  do {
-    if (kCluster ? mbar_try_wait_hint_cluster(bar, parity) : mbar_try_wait_hint(bar, parity)) return true;
-  } while (clock64() - t0 < kWaitLimitCycles);
-  *failed = site << 24 | (detail & 0xffffff);
-  return false;
 }
 
 // Multiply TMEM columns [c0, c1) of the warp's lanes by alpha (it runs only
@@ -127,51 +93,6 @@ __device__ __forceinline__ void scale_o(uint32_t lane_base, int c0, int c1, floa
     tmem_st32(lane_base + c, r);
   }
   tmem_st_wait();
-}
-
-// The cache row that an index entry names (negative: none), unchecked: the
-// value of the slot load is not looked at before checked_row.
-__device__ __forceinline__ int slot_of(const AttnInt4Params &P, int32_t *bad, int entry, int k) {
-  if (!P.slots || entry < 0) return entry;
-  if (entry >= P.num_kv_rows) {
-    bad[0] = 49;
-    bad[1] = k;
-    return -1;
-  }
-  return __ldg(P.slots + entry);
-}
-__device__ __forceinline__ int checked_row(const AttnInt4Params &P, int32_t *bad, int row, int k) {
-  if (row >= P.cache_rows) {
-    bad[0] = 50;
-    bad[1] = k;
-    return -1;
-  }
-  return row;
-}
-
-// Loads of cache bytes, each used once on this SM; volatile, to be issued where they stand.
-__device__ __forceinline__ uint4 ld_once_v4(const void *p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint32_t ld_once_u16(const void *p) {
-  uint16_t r;
-  asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(r) : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint32_t ld_once_u8(const void *p) {
-  uint32_t r;
-  asm volatile("ld.global.nc.L1::no_allocate.u8 %0, [%1];" : "=r"(r) : "l"(p));
-  return r;
-}
-
-// The bulk copy of an O half out of shared memory.
-__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -271,12 +192,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t *bad = misc + 2;     // site and position of an index that was out of range
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const int nb = (last + kBN - 1) / kBN;
-  const int64_t half = static_cast<int64_t>(unit) * 2 + crank;  // of the workspace arrays
+  const int64_t part = static_cast<int64_t>(unit) * P.H;  // of the workspace arrays
   __nv_bfloat16 *out_row = P.out + static_cast<int64_t>(qrow) * P.H * kDv + main_dim0;
 
   if (nb == 0) {
     if (P.splits > 1) {
-      if (tid < P.H) P.part_ml[half * P.H + tid] = make_float2(-__builtin_huge_valf(), 0.f);
+      if (tid < P.H) P.part_ml[2 * (part + tid) + crank] = make_float2(-__builtin_huge_valf(), 0.f);
     } else if (qrow >= 0) {
       for (int u = tid; u < P.H * (kDvc / 8); u += kThreads)
         *reinterpret_cast<uint4 *>(out_row + static_cast<int64_t>(u / (kDvc / 8)) * kDv + u % (kDvc / 8) * 8) =
@@ -382,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // A row's registers are loaded for the next block as soon as this block's
     // row is decoded, so that a freed stage is full again after the decoding
     // alone; slots are fetched one block before that, entries two.  An entry
-    // that names no row reads row 0 with factors of zero.
+    // that names no row reads nothing; its factors are zero.
     const int w = warp - 10, v = lane >> 2, r4 = lane & 3, own = 16 * w + (lane & 15);
     auto entry_of = [&](int j) {
       const int k = j * kBN + own;
@@ -391,17 +312,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint8_t *const lane_codes = P.cache + main_dim0 / 2 + 16 * v;
     const uint8_t *const lane_scales = P.cache + P.g.scales + main_dim0 / 16 + 2 * v;
     uint4 code[4];
-    uint32_t scales[4], exponent;
+    uint32_t scales[4], exponent = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      code[q] = make_uint4(0u, 0u, 0u, 0u);
+      scales[q] = 0;
+    }
     auto load = [&](int q, int rr) {
-      const int64_t at = static_cast<int64_t>(__shfl_sync(0xffffffffu, rr, 4 * q + r4)) * P.g.row_bytes;
-      code[q] = ld_once_v4(lane_codes + at);
-      scales[q] = ld_once_u16(lane_scales + at);
+      const int rw = __shfl_sync(0xffffffffu, rr, 4 * q + r4);
+      const int64_t at = static_cast<int64_t>(max(rw, 0)) * P.g.row_bytes;
+      ld_once(code[q], lane_codes + at, rw >= 0);
+      ld_once_u16(scales[q], lane_scales + at, rw >= 0);
+    };
+    auto load_exponent = [&](int rr) {
+      ld_once_u8(exponent, P.cache + static_cast<int64_t>(max(rr, 0)) * P.g.row_bytes + P.g.exponent, rr >= 0);
     };
     int row = checked_row(P, bad, slot_of(P, bad, entry_of(0), k0 + own), k0 + own);
     int row_next = slot_of(P, bad, entry_of(1), k0 + kBN + own), entry = entry_of(2);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) load(q, max(row, 0));
-    exponent = ld_once_u8(P.cache + static_cast<int64_t>(max(row, 0)) * P.g.row_bytes + P.g.exponent);
+    for (int q = 0; q < 4; ++q) load(q, row);
+    load_exponent(row);
     // the lane's place in a stage for row 4q + r4 and unit u of its four, less 512 q: place[(q & 1) * 4 + u]
     uint32_t place[8];
 #pragma unroll
@@ -412,8 +342,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int s = j % kStages;
       const uint32_t sb = smem_u32(smem + kOffStage + s * kStageBytes);
       const uint32_t used = __ballot_sync(0xffffffffu, row >= 0);
+      const uint32_t factors = row >= 0 ? int4_row_factors(exponent) : 0u;
       row_next = checked_row(P, bad, row_next, k0 + (j + 1) * kBN + own);
-      const int next0 = max(row_next, 0);
+      load_exponent(row_next);
       const int row_after = slot_of(P, bad, entry, k0 + (j + 2) * kBN + own);
       entry = entry_of(j + 3);
       // stages 1 and 2 held the staged Q until the softmax warps moved it to TMEM;
@@ -431,7 +362,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     rw >= 0 ? 16u : 0u);
       }
       cp_async_commit();
-      const uint32_t factors = row >= 0 ? int4_row_factors(exponent) : 0u;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const uint32_t fac = __shfl_sync(0xffffffffu, factors, 4 * q + r4);
@@ -448,9 +378,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(sb + place[(q & 1) * 4 + u] + 512 * q, o[0], o[1], o[2], o[3]);
           }
         }
-        load(q, next0);
+        load(q, row_next);
       }
-      exponent = ld_once_u8(P.cache + static_cast<int64_t>(next0) * P.g.row_bytes + P.g.exponent);
       cp_async_wait<0>();
       fence_proxy_async_smem();
       warp_arrive(&kv_full[s], lane);
@@ -657,8 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     } else {
-      // this split's part: O as it is (fp32), unit u of row h at u ^ (h & 63)
-      // in shared memory and in the workspace alike, one bulk copy of H KB
+      // this split's part: O as it is (fp32), a row's 1 KB through shared memory
+      // (16 bytes apart, so that the row-wise writes do not collide) and one
+      // bulk copy per row
       if (ok) {
 #pragma unroll 1
         for (int c = w * (kDvc / 2); c < (w + 1) * (kDvc / 2); c += 32) {
@@ -666,18 +596,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld32(lane_base + c, r);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const int u = (c + k) >> 2;
-            *reinterpret_cast<uint4 *>(ost + h * 1024 + ((u ^ (h & 63)) << 4)) =
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<uint4 *>(ost + h * kPartRow + (c + k) * 4) =
                 make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
-          }
         }
-        if (w == 0 && h < P.H) P.part_ml[half * P.H + h] = make_float2(m_used, l);
+        if (w == 0 && h < P.H) P.part_ml[2 * (part + h) + crank] = make_float2(m_used, l);
       }
       fence_proxy_async_smem();
       warp_arrive(o_staged, lane);
-      if (tid == 0 && wait_for(o_staged, 0, failed, 76) && ok) {
-        bulk_store(P.part_o + half * P.H * kDvc, ost, static_cast<uint32_t>(P.H) * kDvc * 4);
+      if (w == 0 && wait_for(o_staged, 0, failed, 76) && ok && h < P.H) {
+        bulk_store(P.part_o + (part + h) * kDv + main_dim0, ost + h * kPartRow, kDvc * 4);
         bulk_commit();
         bulk_wait_read0();
       }
@@ -698,32 +626,28 @@ __global__ void __launch_bounds__(kThreads, 1)
 // with m their largest, the sum runs in split order.  One block per (query,
 // head), a thread on four value columns, eight parts' loads in flight; the
 // weights come from one pass of the warps' lanes over the parts' (m, l).
-constexpr int kMaxSplits = 32;
 __global__ void __launch_bounds__(128) sparse_attn_int4_join_kernel(const AttnInt4Params P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel may still run
-  const int query = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31;
+  const int query = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, half = threadIdx.x >> 6;
   const int qrow = P.q_rows ? P.q_rows[query] : query;
   if (qrow < 0 || qrow >= P.num_q_rows) return;  // the latter reported by the first kernel
-  const int crank = threadIdx.x >> 6, u = threadIdx.x & 63;
-  const int64_t first = static_cast<int64_t>(query) * P.splits * 2 + crank;
-  const int64_t step = 2 * static_cast<int64_t>(P.H);  // rows of the same half between splits
+  const int64_t first = static_cast<int64_t>(query) * P.splits * P.H + h;
   float2 t = make_float2(-__builtin_huge_valf(), 0.f);
-  if (lane < P.splits) t = P.part_ml[first * P.H + h + lane * step];
-  float m = t.x;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+  if (lane < P.splits) t = P.part_ml[2 * (first + static_cast<int64_t>(lane) * P.H) + half];
+  const float m = warp_max(t.x);
   const unsigned parts = __ballot_sync(0xffffffffu, t.y != 0.f);  // the others have no entry, and no O was written
   const float wgt = t.y != 0.f ? ex2(t.x - (m == -__builtin_huge_valf() ? 0.f : m)) : 0.f;
   float l = P.sink ? ex2(P.sink[h] * 1.4426950408889634f - m) : 0.f;
   const float wl = t.y != 0.f ? wgt * t.y : 0.f;
-  const float4 *o = reinterpret_cast<const float4 *>(P.part_o + (first * P.H + h) * kDvc) + (u ^ (h & 63));
+  const float4 *o = reinterpret_cast<const float4 *>(P.part_o + first * kDv) + threadIdx.x;
+  const int64_t step = static_cast<int64_t>(P.H) * (kDv / 4);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int s0 = 0; s0 < P.splits; s0 += 8) {
     float4 x[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if ((parts >> (s0 + k)) & 1u) x[k] = o[(s0 + k) * step * (kDvc / 4)];
+      if ((parts >> (s0 + k)) & 1u) x[k] = o[(s0 + k) * step];
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -736,22 +660,22 @@ __global__ void __launch_bounds__(128) sparse_attn_int4_join_kernel(const AttnIn
     }
   }
   const float inv = parts && l != 0.f ? 1.f / l : 0.f;
-  uint2 r = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  *reinterpret_cast<uint2 *>(P.out + (static_cast<int64_t>(qrow) * P.H + h) * kDv + crank * kDvc + 4 * u) = r;
+  const uint2 r = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2 *>(P.out + (static_cast<int64_t>(qrow) * P.H + h) * kDv + 4 * threadIdx.x) = r;
 }
 
-// Entries per split.  A cluster's time is a fixed part (set-up, Q, the first
-// block's chain, the O half) plus one part per block of 64 entries; with s
-// splits there are n * s clusters for the device's SM pairs.
-int splits_for(int64_t n, int topk, int sms) {
-  const int blocks = (topk + kBN - 1) / kBN, pairs = sms / 2 > 0 ? sms / 2 : 1;
+// Splits of a query's entries.  A unit (a CTA of the kernel for few heads, a
+// pair of the other) takes a fixed time (set-up, Q, the first block's chain,
+// O) and a time per block; `fixed` is the former in blocks, and `join` what the
+// second kernel costs.  n * s units share `units` places.
+int splits_for(int64_t n, int blocks, int units, double fixed, double join) {
   int best = 1;
   double best_cost = 1e300;
-  for (int s = 1; s <= blocks && s <= kMaxSplits; ++s) {
+  for (int s = 1; s <= blocks && s <= kInt4MaxSplits; ++s) {
     const int per = (blocks + s - 1) / s;
     if ((blocks + per - 1) / per != s) continue;  // the same division as a smaller s
-    const double waves = static_cast<double>((n * s + pairs - 1) / pairs);
-    const double cost = waves * (5.0 + per) + (s > 1 ? 3.0 + 0.03 * static_cast<double>(n * s) : 0.0);
+    const double waves = static_cast<double>((n * s + units - 1) / units);
+    const double cost = waves * (fixed + per) + (s > 1 ? join * (1.0 + 0.005 * static_cast<double>(n * s)) : 0.0);
     if (cost < best_cost) {
       best_cost = cost;
       best = s;
@@ -760,20 +684,61 @@ int splits_for(int64_t n, int topk, int sms) {
   return best;
 }
 
+struct Division {
+  int splits, split_len;
+};
+Division divide(int64_t n, int H, int topk) {
+  const bool few = H <= kInt4FewHeads;
+  const int rows = few ? kInt4FewRows : kBN, blocks = (topk + rows - 1) / rows;
+  const int sms = num_sms(), units = few ? sms : sms > 1 ? sms / 2 : 1;
+  const int s = splits_for(n, blocks, units, few ? 3.0 : 5.0, few ? 2.0 : 3.0);
+  return {s, (blocks + s - 1) / s * rows};
+}
+
+size_t part_bytes(int64_t n, int splits, int H) {
+  return splits > 1 ? static_cast<size_t>(n) * splits * H * (kDv * 4 + 16) : 0;
+}
+
+dsa_status launch_pairs(const void *q, int32_t n, const AttnInt4Params &P, cudaStream_t stream) {
+  CUtensorMap qmain, qtail;
+  const uint64_t dims[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(P.H), static_cast<uint64_t>(P.num_q_rows)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(kD) * 2, static_cast<uint64_t>(P.H) * kD * 2};
+  const uint32_t box_main[3] = {64, kHeads, 1}, box_tail[3] = {32, kHeads, 1};
+  dsa_status st = encode_tensor_map(&qmain, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box_main,
+                                    CU_TENSOR_MAP_SWIZZLE_128B);
+  if (st != DSA_OK) return st;
+  st = encode_tensor_map(&qtail, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box_tail,
+                         CU_TENSOR_MAP_SWIZZLE_64B);
+  if (st != DSA_OK) return st;
+  cudaError_t e = cudaFuncSetAttribute(sparse_attn_int4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  if (e != cudaSuccess) return cuda_fail(e);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(n) * P.splits * 2u);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_kernel, qmain, qtail, P);
+  if (e != cudaSuccess) return cuda_fail(e);
+  return check_launch();
+}
+
 }  // namespace
 }  // namespace dsa
 
 using namespace dsa;
 
-static size_t part_bytes(int64_t n, int splits, int H) {
-  return splits > 1 ? static_cast<size_t>(n) * splits * 2 * H * (kDvc * 4 + 8) : 0;
-}
-
 extern "C" dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t topk, size_t *bytes) {
   if (!bytes) return DSA_ERR_INVALID_ARG;
   if (n < 0 || topk < 1) return DSA_ERR_SHAPE;
   if (H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
-  *bytes = n == 0 ? 0 : part_bytes(n, splits_for(n, topk, num_sms()), H);
+  *bytes = n == 0 ? 0 : part_bytes(n, divide(n, H, topk).splits, H);
   return DSA_OK;
 }
 
@@ -790,10 +755,10 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   if (n == 0 || num_q_rows == 0) return DSA_OK;
   if (!q || !kv_cache || !topk_idx || !out) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
-  const int splits = splits_for(n, topk, num_sms());
-  const size_t need = part_bytes(n, splits, H);
+  const Division div = divide(n, H, topk);
+  const size_t need = part_bytes(n, div.splits, H);
   if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return DSA_ERR_WORKSPACE;
-  if (static_cast<int64_t>(n) * splits * 2 > INT32_MAX) return DSA_ERR_SHAPE;
+  if (static_cast<int64_t>(n) * div.splits * 2 > INT32_MAX) return DSA_ERR_SHAPE;
   int *err = device_error_word();
   if (!err) return DSA_ERR_CUDA;
 
@@ -805,14 +770,13 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   P.sink = attn_sink;
   P.out = static_cast<__nv_bfloat16 *>(out);
   P.part_o = static_cast<float *>(workspace);
-  P.part_ml = reinterpret_cast<float2 *>(static_cast<float *>(workspace) +
-                                         static_cast<int64_t>(n) * splits * 2 * H * kDvc);
+  P.part_ml =
+      reinterpret_cast<float2 *>(static_cast<float *>(workspace) + static_cast<int64_t>(n) * div.splits * H * kDv);
   P.scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * 1.4426950408889634);
   P.H = H;
   P.topk = topk;
-  P.splits = splits;
-  const int blocks = (topk + kBN - 1) / kBN;
-  P.split_len = (blocks + splits - 1) / splits * kBN;
+  P.splits = div.splits;
+  P.split_len = div.split_len;
   P.num_kv_rows = num_kv_rows;
   P.cache_rows = num_cache_rows;
   P.num_q_rows = num_q_rows;
@@ -820,40 +784,19 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   if (st != DSA_OK) return st;
   P.err = err;
 
-  CUtensorMap qmain, qtail;
-  const uint64_t dims[3] = {static_cast<uint64_t>(kD), static_cast<uint64_t>(H), static_cast<uint64_t>(num_q_rows)};
-  const uint64_t strides[2] = {static_cast<uint64_t>(kD) * 2, static_cast<uint64_t>(H) * kD * 2};
-  const uint32_t box_main[3] = {64, kHeads, 1}, box_tail[3] = {32, kHeads, 1};
-  st = encode_tensor_map(&qmain, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box_main,
-                         CU_TENSOR_MAP_SWIZZLE_128B);
-  if (st != DSA_OK) return st;
-  st = encode_tensor_map(&qtail, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box_tail,
-                         CU_TENSOR_MAP_SWIZZLE_64B);
-  if (st != DSA_OK) return st;
-  cudaError_t e = cudaFuncSetAttribute(sparse_attn_int4_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return cuda_fail(e);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  st = H <= kInt4FewHeads ? launch_attn_int4_few(q, n, P, s) : launch_pairs(q, n, P, s);
+  if (st != DSA_OK || div.splits == 1) return st;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n) * splits * 2u);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.gridDim = dim3(static_cast<unsigned>(n), static_cast<unsigned>(H));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_kernel, qmain, qtail, P);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_join_kernel, P);
   if (e != cudaSuccess) return cuda_fail(e);
-  if (splits > 1) {
-    cfg.gridDim = dim3(static_cast<unsigned>(n), static_cast<unsigned>(H));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_join_kernel, P);
-    if (e != cudaSuccess) return cuda_fail(e);
-  }
   return check_launch();
 }

@@ -51,6 +51,7 @@ constexpr int kStages = 4;
 constexpr int kNMain = 4;            // 64-wide latent chunks per CTA (128B swizzle), plus one of 32 (64B swizzle)
 constexpr int kDvc = 256;            // value columns per CTA
 constexpr int kThreads = 448;
+constexpr int kFirstGatherWarp = 10;
 constexpr int kQMain = kNMain * 128 * 128, kQTail = 128 * 64;
 constexpr int kStageMain = kNMain * kBN * 128, kStageBytes = kStageMain + kBN * 64;
 constexpr int kQKMainSteps = kNMain * 4, kQKSteps = kQKMainSteps + 2, kPVSteps = kBN / 16;
@@ -175,6 +176,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), kTmemCols);
     tmem_relinquish();
   }
+  // The gather starts here already (roles below): three dependent loads, entry,
+  // slot and row, run while the rest is set up.  Lane l of gather warp w knows
+  // row 16w + l % 16 of a block, and loads for row 4q + r4 of it.
+  const int own = 16 * (warp - kFirstGatherWarp) + (lane & 15), v = lane >> 2, r4 = lane & 3;
+  const uint8_t *const lane_codes = P.cache + main_dim0 / 2 + 16 * v;
+  const uint8_t *const lane_scales = P.cache + P.g.scales + main_dim0 / 16 + 2 * v;
+  int row = -1, row_next = -1, entry = -1;
+  uint4 code[4];
+  uint32_t scales[4], exponent = 0;
+  auto entry_of = [&](int j) {
+    const int k = k0 + j * kBN + own;
+    return q_issued && k < k1 ? __ldg(idx_row + k) : -1;
+  };
+  auto load = [&](int q, int rr) {
+    const int rw = __shfl_sync(0xffffffffu, rr, 4 * q + r4);
+    const int64_t at = static_cast<int64_t>(max(rw, 0)) * P.g.row_bytes;
+    ld_once(code[q], lane_codes + at, rw >= 0);
+    ld_once_u16(scales[q], lane_scales + at, rw >= 0);
+  };
+  auto load_exponent = [&](int rr) {
+    ld_once_u8(exponent, P.cache + static_cast<int64_t>(max(rr, 0)) * P.g.row_bytes + P.g.exponent, rr >= 0);
+  };
+  int32_t early_bad[2] = {0, 0};  // an index out of range, before shared memory is set up
+  if (warp >= kFirstGatherWarp) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      code[q] = make_uint4(0u, 0u, 0u, 0u);
+      scales[q] = 0;
+    }
+    row = entry_of(0);
+    row_next = entry_of(1);
+    entry = entry_of(2);
+    row = checked_row(P, early_bad, slot_of(P, early_bad, row, k0 + own), k0 + own);
+    row_next = slot_of(P, early_bad, row_next, k0 + kBN + own);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) load(q, row);
+    load_exponent(row);
+  }
   // one past the split's last entry that names a row: the blocks behind it are skipped
   int last = 0;
   if (q_issued)
@@ -205,29 +244,34 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (q_issued) wait_for(q_full, 0, failed, 60);  // the Q load issued at the start has landed
   } else if (warp == 8) {
-    if (lane == 0) {
-      // ---------------- MMA issuer, event-driven: QK(j) as soon as its rows are
-      // there, its S buffer is free and PV(j - 3) has been issued, PV(i) as
-      // soon as P(i) is written; each stream in order
-      const uint32_t st_addr = smem_u32(smem + kOffStage);
-      const uint64_t qk_b0 = smem_desc(st_addr, 16, 1024, kLayoutSW128);
-      const uint64_t qk_t0 = smem_desc(st_addr + kStageMain, 16, 512, kLayoutSW64);
-      const uint64_t qt_a0 = smem_desc(smem_u32(smem + kOffQTail), 16, 512, kLayoutSW64);
-      const uint64_t pv_a0 = smem_desc(smem_u32(smem + kOffRecv), 16, 1024, kLayoutSW128);
-      const uint64_t pv_b0 = smem_desc(st_addr, kBN * 128, 1024, kLayoutSW128);
-      const uint32_t s_tm = tmem + kSCol, q_tm = tmem + kQCol;
-      bool ok = wait_for(q_full, 0, failed, 61) && wait_for(q_ready, 0, failed, 61);
-      tc_fence_after();
-      int qk = 0, pv = 0;
-      long long t_prog = clock64(), t_check = t_prog;
-      while (ok && pv < nb) {
-        bool progressed = false;
-        if (qk < nb && qk < pv + 3 && mbar_test(&kv_full[qk % kStages], (qk / kStages) & 1) &&
-            (qk < 2 || mbar_test(&s_free[qk & 1], ((qk - 2) >> 1) & 1))) {
-          tc_fence_after();
-          const uint32_t d = s_tm + (qk & 1) * kBN;
-          const uint32_t so = static_cast<uint32_t>((qk % kStages) * kStageBytes) >> 4;
-          const uint64_t kb = desc_add(qk_b0, so), kt = desc_add(qk_t0, so);
+    // ---------------- MMA issuer, event-driven: QK(j) as soon as its rows are
+    // there, its S buffer is free and PV(j - 3) has been issued, PV(i) as soon as
+    // P(i) is written; each stream in order.  The whole warp runs the loop and
+    // one elected lane issues: descriptors and addresses then live in uniform
+    // registers (the least an MMA takes is 45 cycles so; 63 from a branch of one
+    // lane).
+    const bool issuer = elect_one();
+    const uint32_t st_addr = smem_u32(smem + kOffStage);
+    const uint64_t qk_b0 = smem_desc(st_addr, 16, 1024, kLayoutSW128);
+    const uint64_t qk_t0 = smem_desc(st_addr + kStageMain, 16, 512, kLayoutSW64);
+    const uint64_t qt_a0 = smem_desc(smem_u32(smem + kOffQTail), 16, 512, kLayoutSW64);
+    const uint64_t pv_a0 = smem_desc(smem_u32(smem + kOffRecv), 16, 1024, kLayoutSW128);
+    const uint64_t pv_b0 = smem_desc(st_addr, kBN * 128, 1024, kLayoutSW128);
+    const uint32_t s_tm = tmem + kSCol, q_tm = tmem + kQCol;
+    bool ok = __all_sync(0xffffffffu, wait_for(q_full, 0, failed, 61) && wait_for(q_ready, 0, failed, 61));
+    tc_fence_after();
+    int qk = 0, pv = 0;
+    long long t_prog = clock64();
+    while (ok && pv < nb) {
+      bool progressed = false;
+      if (qk < nb && qk < pv + 3 &&
+          __all_sync(0xffffffffu, mbar_test(&kv_full[qk % kStages], (qk / kStages) & 1) &&
+                                      (qk < 2 || mbar_test(&s_free[qk & 1], ((qk - 2) >> 1) & 1)))) {
+        tc_fence_after();
+        const uint32_t d = s_tm + (qk & 1) * kBN;
+        const uint32_t so = static_cast<uint32_t>((qk % kStages) * kStageBytes) >> 4;
+        const uint64_t kb = desc_add(qk_b0, so), kt = desc_add(qk_t0, so);
+        if (issuer) {
 #pragma unroll
           for (int k = 0; k < kQKSteps; ++k) {
             if (k < kQKMainSteps) {
@@ -239,32 +283,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           mma_commit(&s_full[qk & 1]);
-          ++qk;
-          progressed = true;
         }
-        if (pv < qk && mbar_test(&p_full[pv & 1], (pv >> 1) & 1)) {
-          tc_fence_after();
-          const int bi = pv & 1, si = pv % kStages;
-          const uint64_t vb = desc_add(pv_b0, static_cast<uint32_t>(si * kStageBytes) >> 4);
-          const uint64_t pb = desc_add(pv_a0, static_cast<uint32_t>(bi * kRecvBytes) >> 4);
+        __syncwarp();
+        ++qk;
+        progressed = true;
+      }
+      if (pv < qk && __all_sync(0xffffffffu, mbar_test(&p_full[pv & 1], (pv >> 1) & 1))) {
+        tc_fence_after();
+        const int bi = pv & 1, si = pv % kStages;
+        const uint64_t vb = desc_add(pv_b0, static_cast<uint32_t>(si * kStageBytes) >> 4);
+        const uint64_t pb = desc_add(pv_a0, static_cast<uint32_t>(bi * kRecvBytes) >> 4);
+        if (issuer) {
 #pragma unroll
           for (int k = 0; k < kPVSteps; ++k)
             mma_ss(tmem, desc_add(pb, k * 2), desc_add(vb, k * 128), kIdescPV, (pv > 0 || k > 0) ? 1u : 0u);
           mma_commit(&pv_done[bi]);
           mma_commit(&kv_empty[si]);
-          ++pv;
-          progressed = true;
         }
-        const long long now = clock64();
-        if (progressed) {
-          t_prog = now;
-        } else if (now - t_check > 100000) {
-          t_check = now;
-          if (now - t_prog > kWaitLimitCycles) {
-            *failed = 62 << 24 | (pv & 0xffffff);
-            ok = false;
-          }
-        }
+        __syncwarp();
+        ++pv;
+        progressed = true;
+      }
+      const long long now = clock64();
+      if (progressed) {
+        t_prog = now;
+      } else if (__any_sync(0xffffffffu, now - t_prog > kWaitLimitCycles)) {
+        *failed = 62 << 24 | (pv & 0xffffff);
+        ok = false;
       }
     }
   } else if (warp == 9) {
@@ -293,7 +338,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       bulk_wait_read0();
     }
-  } else if (warp >= 10) {
+  } else if (warp >= kFirstGatherWarp) {
+    if (early_bad[0]) {
+      bad[0] = early_bad[0];
+      bad[1] = early_bad[1];
+    }
     // ---------------- gather: four warps, one on each sub-partition, so that
     // none of the softmax warps shares its issue slots with more decoding than
     // the others; warp w takes rows 16w .. 16w + 15 of every block.  Lane l
@@ -304,34 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // row is decoded, so that a freed stage is full again after the decoding
     // alone; slots are fetched one block before that, entries two.  An entry
     // that names no row reads nothing; its factors are zero.
-    const int w = warp - 10, v = lane >> 2, r4 = lane & 3, own = 16 * w + (lane & 15);
-    auto entry_of = [&](int j) {
-      const int k = j * kBN + own;
-      return j < nb && k < last ? __ldg(idx_row + k0 + k) : -1;
-    };
-    const uint8_t *const lane_codes = P.cache + main_dim0 / 2 + 16 * v;
-    const uint8_t *const lane_scales = P.cache + P.g.scales + main_dim0 / 16 + 2 * v;
-    uint4 code[4];
-    uint32_t scales[4], exponent = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      code[q] = make_uint4(0u, 0u, 0u, 0u);
-      scales[q] = 0;
-    }
-    auto load = [&](int q, int rr) {
-      const int rw = __shfl_sync(0xffffffffu, rr, 4 * q + r4);
-      const int64_t at = static_cast<int64_t>(max(rw, 0)) * P.g.row_bytes;
-      ld_once(code[q], lane_codes + at, rw >= 0);
-      ld_once_u16(scales[q], lane_scales + at, rw >= 0);
-    };
-    auto load_exponent = [&](int rr) {
-      ld_once_u8(exponent, P.cache + static_cast<int64_t>(max(rr, 0)) * P.g.row_bytes + P.g.exponent, rr >= 0);
-    };
-    int row = checked_row(P, bad, slot_of(P, bad, entry_of(0), k0 + own), k0 + own);
-    int row_next = slot_of(P, bad, entry_of(1), k0 + kBN + own), entry = entry_of(2);
-#pragma unroll
-    for (int q = 0; q < 4; ++q) load(q, row);
-    load_exponent(row);
+    const int w = warp - kFirstGatherWarp;
     // the lane's place in a stage for row 4q + r4 and unit u of its four, less 512 q: place[(q & 1) * 4 + u]
     uint32_t place[8];
 #pragma unroll

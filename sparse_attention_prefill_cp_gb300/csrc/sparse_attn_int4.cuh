@@ -44,6 +44,13 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // mbar_wait without a call, for the loops that hold most of the registers:
 // bounded by the same time, the failing site and detail noted in shared memory.
 template <bool kCluster = false>

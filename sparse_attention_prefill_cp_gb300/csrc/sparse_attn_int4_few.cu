@@ -77,12 +77,6 @@ struct FewCfg {
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
 
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
 // OR of a predicate over the softmax warps, and a barrier among them.
 __device__ __forceinline__ bool softmax_or(bool p) {
   uint32_t r;
@@ -182,6 +176,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), C::kTmemCols);
     tmem_relinquish();
   }
+  // Decoding and rope copies start here already (roles below): three dependent
+  // loads, entry, slot and row, run while the rest is set up.
+  const int decoder = warp - kFirstDecodeWarp;
+  const int own = decoder >= 0 ? kWarpRows * decoder + (lane & 15) : tid;  // the lane's row of a block
+  auto entry_of = [&](int j) {
+    const int k = k0 + j * kRows + own;
+    return q_issued && k < k1 ? __ldg(idx_row + k) : -1;
+  };
+  // decoding: four lanes copy a row's 64 bytes of codes of tile t, for rows lane / 4 and 8 + lane / 4 of the warp
+  uint8_t *const raw = smem + C::kOffRaw + kWarpRows * decoder * kRawRow;
+  const uint32_t raw_to = smem_u32(raw) + (lane >> 2) * kRawRow + 16 * (lane & 3);
+  const uint8_t *const raw_from = P.cache + 16 * (lane & 3);
+  auto copy = [&](int t, int row0, int row1) {
+    cp_async_16(raw_to + 64 * t, raw_from + static_cast<int64_t>(max(row0, 0)) * P.g.row_bytes + 64 * t,
+                row0 >= 0 ? 16u : 0u);
+    cp_async_16(raw_to + 64 * t + 8 * kRawRow, raw_from + static_cast<int64_t>(max(row1, 0)) * P.g.row_bytes + 64 * t,
+                row1 >= 0 ? 16u : 0u);
+    cp_async_commit();
+  };
+  uint4 scales = make_uint4(0u, 0u, 0u, 0u);  // half (lane >> 4) of row lane % 16
+  uint32_t exponent = 0;
+  auto load = [&](int rr) {
+    const uint8_t *src = P.cache + static_cast<int64_t>(max(rr, 0)) * P.g.row_bytes;
+    ld_once(scales, src + P.g.scales + 16 * (lane >> 4), rr >= 0);
+    ld_once_u8(exponent, src + P.g.exponent, rr >= 0);
+  };
+  // softmax: the rope columns of the block whose rows are in `row`, eight lanes a row
+  int row = -1, row_next = -1, entry = -1;
+  const uint32_t rope_tile = smem_u32(smem + C::kOffRope);
+  auto rope_copy = [&]() {
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int rl = 4 * x + (lane >> 3), r = 32 * warp + rl, u = lane & 7;
+      const int rw = __shfl_sync(0xffffffffu, row, rl);
+      cp_async_16(rope_tile + r * 128 + ((u ^ (r & 7)) << 4),
+                  P.cache + static_cast<int64_t>(max(rw, 0)) * P.g.row_bytes + P.g.rope + 16 * u, rw >= 0 ? 16u : 0u);
+    }
+    cp_async_commit();
+  };
+  int32_t early_bad[2] = {0, 0};  // an index out of range, before shared memory is set up
+  if (warp != 4) {
+    row = entry_of(0);
+    row_next = entry_of(1);
+    entry = entry_of(2);
+    row = checked_row(P, early_bad, slot_of(P, early_bad, row, k0 + own), k0 + own);
+    row_next = slot_of(P, early_bad, row_next, k0 + kRows + own);
+    if (decoder >= 0) {
+      load(row);
+      const int row0 = __shfl_sync(0xffffffffu, row, lane >> 2), row1 = __shfl_sync(0xffffffffu, row, 8 + (lane >> 2));
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) copy(t, row0, row1);
+    } else {
+      rope_copy();
+    }
+  }
   // one past the split's last entry that names a row: the blocks behind it are skipped
   int last = 0;
   if (q_issued)
@@ -195,16 +244,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
   for (int i = 0; i < kThreads / 32; ++i) last = max(last, last_used[i]);
 
+  if (early_bad[0]) {
+    bad[0] = early_bad[0];
+    bad[1] = early_bad[1];
+  }
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const int nb = (last + kRows - 1) / kRows;
   const int64_t part = static_cast<int64_t>(unit) * P.H;  // of the workspace arrays
   __nv_bfloat16 *out = P.out + static_cast<int64_t>(qrow) * P.H * kDv;
-
-  // index entry of row r of block j of the split, -1 behind the last
-  auto entry_of = [&](int j, int r) {
-    const int k = j * kRows + r;
-    return j < nb && k < last ? __ldg(idx_row + k0 + k) : -1;
-  };
 
   if (nb == 0) {
     if (P.splits > 1) {
@@ -214,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *reinterpret_cast<uint4 *>(out + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
     }
     if (q_issued) wait_for(q_full, 0, failed, 60);  // the Q load issued at the start has landed
+    cp_async_wait<0>();
   } else if (warp == 4) {
     // ---------------- MMA issuer, in a fixed order: QK of a block tile by tile
     // as they are decoded, then PV, which hands the tiles back one by one.  The
@@ -290,33 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // groups.  A tile's codes are copied for the next block as soon as they are
     // decoded; slots are fetched one block before that, entries two.  An entry
     // that names no row reads nothing; its factors are zero.
-    const int w = warp - kFirstDecodeWarp, v = lane >> 3, r8 = lane & 7, own = kWarpRows * w + (lane & 15);
-    uint8_t *const raw = smem + C::kOffRaw + kWarpRows * w * kRawRow;
-    const uint32_t raw_to = smem_u32(raw) + (lane >> 2) * kRawRow + 16 * (lane & 3);
-    const uint8_t *const raw_from = P.cache + 16 * (lane & 3);
-    // four lanes copy a row's 64 bytes of codes of tile t
-    auto copy = [&](int t, int row0, int row1) {
-      cp_async_16(raw_to + 64 * t, raw_from + static_cast<int64_t>(max(row0, 0)) * P.g.row_bytes + 64 * t,
-                  row0 >= 0 ? 16u : 0u);
-      cp_async_16(raw_to + 64 * t + 8 * kRawRow, raw_from + static_cast<int64_t>(max(row1, 0)) * P.g.row_bytes + 64 * t,
-                  row1 >= 0 ? 16u : 0u);
-      cp_async_commit();
-    };
-    uint4 scales = make_uint4(0u, 0u, 0u, 0u);  // half (lane >> 4) of row lane % 16
-    uint32_t exponent = 0;
-    auto load = [&](int rr) {
-      const uint8_t *src = P.cache + static_cast<int64_t>(max(rr, 0)) * P.g.row_bytes;
-      ld_once(scales, src + P.g.scales + 16 * (lane >> 4), rr >= 0);
-      ld_once_u8(exponent, src + P.g.exponent, rr >= 0);
-    };
-    int row = checked_row(P, bad, slot_of(P, bad, entry_of(0, own), k0 + own), k0 + own);
-    int row_next = slot_of(P, bad, entry_of(1, own), k0 + kRows + own), entry = entry_of(2, own);
-    load(row);
-    {
-      const int row0 = __shfl_sync(0xffffffffu, row, lane >> 2), row1 = __shfl_sync(0xffffffffu, row, 8 + (lane >> 2));
-#pragma unroll
-      for (int t = 0; t < kTiles; ++t) copy(t, row0, row1);
-    }
+    const int w = warp - kFirstDecodeWarp, v = lane >> 3, r8 = lane & 7;
     // the lane's place in a tile for its row 16w + r8 and unit u of its four; the other row is 1024 bytes on
     uint32_t place[4];
 #pragma unroll
@@ -328,7 +350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int j = 0; ok && j < nb; ++j) {
       row_next = checked_row(P, bad, row_next, k0 + (j + 1) * kRows + own);
       const int row_after = slot_of(P, bad, entry, k0 + (j + 2) * kRows + own);
-      entry = entry_of(j + 3, own);
+      entry = entry_of(j + 3);
       const uint32_t factors = row >= 0 ? int4_row_factors(exponent) : 0u;
       const uint32_t fac[2] = {__shfl_sync(0xffffffffu, factors, r8), __shfl_sync(0xffffffffu, factors, 8 + r8)};
       *reinterpret_cast<uint4 *>(raw + (lane & 15) * kRawRow + kRawCodes + 16 * (lane >> 4)) = scales;
@@ -388,25 +410,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; k < HP; ++k) l[k] = 0.f;
     const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
     uint8_t *prow = smem + C::kOffRope + tid * 128;
-    const uint32_t rope_tile = smem_u32(smem + C::kOffRope);
-    int row = checked_row(P, bad, slot_of(P, bad, entry_of(0, tid), k0 + tid), k0 + tid);
-    int row_next = slot_of(P, bad, entry_of(1, tid), k0 + kRows + tid), entry = entry_of(2, tid);
-    auto rope = [&]() {  // of the block whose rows are in `row`, eight lanes a row
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        const int rl = 4 * x + (lane >> 3), r = 32 * warp + rl, u = lane & 7;
-        const int rw = __shfl_sync(0xffffffffu, row, rl);
-        cp_async_16(rope_tile + r * 128 + ((u ^ (r & 7)) << 4),
-                    P.cache + static_cast<int64_t>(max(rw, 0)) * P.g.row_bytes + P.g.rope + 16 * u,
-                    rw >= 0 ? 16u : 0u);
-      }
-      cp_async_commit();
+    auto rope_done = [&]() {
       cp_async_wait<0>();
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(rope_full);
     };
-    rope();
+    rope_done();
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < nb; ++i) {
@@ -502,12 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&s_free[i & 1]);
         mbar_arrive(p_full);
       }
-      row = checked_row(P, bad, row_next, k0 + (i + 1) * kRows + tid);
-      row_next = slot_of(P, bad, entry, k0 + (i + 2) * kRows + tid);
-      entry = entry_of(i + 3, tid);
+      row = checked_row(P, bad, row_next, k0 + (i + 1) * kRows + own);
+      row_next = slot_of(P, bad, entry, k0 + (i + 2) * kRows + own);
+      entry = entry_of(i + 3);
       ok = __all_sync(0xffffffffu, wait_for(pv_done, i & 1, failed, 70, i));
       tc_fence_after();
-      if (ok && i + 1 < nb) rope();
+      if (ok && i + 1 < nb) {
+        rope_copy();
+        rope_done();
+      }
     }
     ok = !softmax_or(!ok);
     if (ok) {

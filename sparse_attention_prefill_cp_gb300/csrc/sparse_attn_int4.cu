@@ -478,17 +478,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (i + 1 < nb) {
         // fetch and ship block i+1 ahead: the peer has it by the time it starts block i+1
         const int b1 = (i + 1) & 1;
-        ok = __all_sync(0xffffffffu, wait_for(&s_full[b1], ((i + 1) >> 1) & 1, failed, 69, i + 1) &&
-                                         (i < 1 || wait_for(&stg_free[b1], ((i - 1) >> 1) & 1, failed, 70, i + 1)));
+        const bool tile_free = i < 1 || mbar_try_wait_hint(&stg_free[b1], ((i - 1) >> 1) & 1);
+        ok = wait_for(&s_full[b1], ((i + 1) >> 1) & 1, failed, 69, i + 1);
+        if (!tile_free) ok = ok && wait_for(&stg_free[b1], ((i - 1) >> 1) & 1, failed, 70, i + 1);
+        ok = __all_sync(0xffffffffu, ok);
         if (!ok) return false;
         tc_fence_after();
         load_s(i + 1, nxt);
         stage(i + 1, nxt);
       }
       if (tid == 0) mbar_arrive_expect_tx(&recv_full[b], kRecvBytes);
-      // the block's rows were complete before its QK; waiting on their barrier too orders the mask word read below
-      ok = __all_sync(0xffffffffu, wait_for<true>(&recv_full[b], (i >> 1) & 1, failed, 71, i) &&
-                                       wait_for(&kv_full[i % kStages], (i / kStages) & 1, failed, 71, i));
+      // the block's rows were complete before its QK; their barrier too orders the mask word read below, and is
+      // asked first, its answer's latency hidden behind the other's
+      const bool rows_full = mbar_try_wait_hint(&kv_full[i % kStages], (i / kStages) & 1);
+      ok = wait_for<true>(&recv_full[b], (i >> 1) & 1, failed, 71, i);
+      if (!rows_full) ok = ok && wait_for(&kv_full[i % kStages], (i / kStages) & 1, failed, 71, i);
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) return false;
       const uint8_t *my_recv = recv0 + b * kRecvBytes + h * 128;
 #pragma unroll
@@ -644,77 +649,48 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync();  // no CTA leaves while its peer may still touch its smem
 }
 
-// Join the splits of one query and head: the parts' weights are e^(m_s - m)
-// with m their largest, the sum runs in split order.  One block per (query,
-// head), a thread on four value columns, eight parts' loads in flight; the
-// weights come from one pass of the warps' lanes over the parts' (m, l).
-__global__ void __launch_bounds__(128) sparse_attn_int4_join_kernel(const AttnInt4Params P) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel may still run
-  const int query = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, half = threadIdx.x >> 6;
-  const int qrow = P.q_rows ? P.q_rows[query] : query;
-  if (qrow < 0 || qrow >= P.num_q_rows) return;  // the latter reported by the first kernel
-  const int64_t first = static_cast<int64_t>(query) * P.splits * P.H + h;
-  float2 t = make_float2(-__builtin_huge_valf(), 0.f);
-  if (lane < P.splits) t = P.part_ml[2 * (first + static_cast<int64_t>(lane) * P.H) + half];
-  const float m = warp_max(t.x);
-  const unsigned parts = __ballot_sync(0xffffffffu, t.y != 0.f);  // the others have no entry, and no O was written
-  const float wgt = t.y != 0.f ? ex2(t.x - (m == -__builtin_huge_valf() ? 0.f : m)) : 0.f;
-  float l = P.sink ? ex2(P.sink[h] * 1.4426950408889634f - m) : 0.f;
-  const float wl = t.y != 0.f ? wgt * t.y : 0.f;
-  const float4 *o = reinterpret_cast<const float4 *>(P.part_o + first * kDv) + threadIdx.x;
-  const int64_t step = static_cast<int64_t>(P.H) * (kDv / 4);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < P.splits; s0 += 8) {
-    float4 x[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if ((parts >> (s0 + k)) & 1u) x[k] = o[(s0 + k) * step];
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float w = __shfl_sync(0xffffffffu, wgt, s0 + k);
-      l += __shfl_sync(0xffffffffu, wl, s0 + k);
-      acc.x += w * x[k].x;
-      acc.y += w * x[k].y;
-      acc.z += w * x[k].z;
-      acc.w += w * x[k].w;
-    }
-  }
-  const float inv = parts && l != 0.f ? 1.f / l : 0.f;
-  const uint2 r = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-  *reinterpret_cast<uint2 *>(P.out + (static_cast<int64_t>(qrow) * P.H + h) * kDv + 4 * threadIdx.x) = r;
-}
+// How a call is divided: over CTA pairs with all heads (this file), or over
+// single CTAs with groups of 16 or 32 heads (sparse_attn_int4_few.cu), and over
+// splits of a query's entries.  The times below are what the kernels took, in
+// us, for 1 to 256 queries of 2048 entries in 1 to 32 splits, to about 10 %:
+//   a wave of pairs        9 + 1.5 per block of  64 entries (any number of heads)
+//   a wave of 16-head CTAs 4 + 3.7 per block of 128
+//   a wave of 32-head CTAs 4.5 + 4.1 per block of 128
+//   joining splits         3 + the parts written and read at 5 TB/s
+// Pairs win where there are many heads and enough queries for the SMs (128
+// heads: 64 queries 60 us, against 150 in groups); groups win up to 32 heads
+// (16 heads: 37 against 60) and for a query or two of many heads, whose splits
+// alone do not fill the SMs.
+struct Division {
+  int splits, split_len, group_heads;  // group_heads 0: pairs
+};
 
-// Splits of a query's entries.  A unit (a CTA of the kernel for few heads, a
-// pair of the other) takes a fixed time (set-up, Q, the first block's chain,
-// O) and a time per block; `fixed` is the former in blocks, and `join` what the
-// second kernel costs.  n * s units share `units` places.
-int splits_for(int64_t n, int blocks, int units, double fixed, double join) {
-  int best = 1;
+Division divide(int64_t n, int H, int topk) {
+  struct Way {
+    int group_heads, rows;
+    double fixed, block;
+  };
+  const Way ways[3] = {{0, kBN, 9.0, 1.5}, {16, kInt4FewRows, 4.0, 3.7}, {32, kInt4FewRows, 4.5, 4.1}};
+  const int sms = num_sms();
+  Division best{1, 0, 0};
   double best_cost = 1e300;
-  for (int s = 1; s <= blocks && s <= kInt4MaxSplits; ++s) {
-    const int per = (blocks + s - 1) / s;
-    if ((blocks + per - 1) / per != s) continue;  // the same division as a smaller s
-    const double waves = static_cast<double>((n * s + units - 1) / units);
-    const double cost = waves * (fixed + per) + (s > 1 ? join * (1.0 + 0.005 * static_cast<double>(n * s)) : 0.0);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = s;
+  for (const Way &w : ways) {
+    const int blocks = (topk + w.rows - 1) / w.rows;
+    const int groups = w.group_heads ? (H + w.group_heads - 1) / w.group_heads : 1;
+    const int units = w.group_heads ? sms : sms > 1 ? sms / 2 : 1;
+    for (int s = 1; s <= blocks && s <= kInt4MaxSplits; ++s) {
+      const int per = (blocks + s - 1) / s;
+      if ((blocks + per - 1) / per != s) continue;  // the same division as a smaller s
+      const double waves = static_cast<double>((n * s * groups + units - 1) / units);
+      const double parts = static_cast<double>(n * s) * H * (2 * kDv * 4) / 5e6;
+      const double cost = waves * (w.fixed + w.block * per) + (s > 1 ? 3.0 + parts : 0.0);
+      if (cost < best_cost) {
+        best_cost = cost;
+        best = {s, per * w.rows, w.group_heads};
+      }
     }
   }
   return best;
-}
-
-struct Division {
-  int splits, split_len;
-};
-Division divide(int64_t n, int H, int topk) {
-  const bool few = H <= kInt4FewHeads;
-  const int rows = few ? kInt4FewRows : kBN, blocks = (topk + rows - 1) / rows;
-  const int sms = num_sms(), units = few ? sms : sms > 1 ? sms / 2 : 1;
-  const int s = splits_for(n, blocks, units, few ? 3.0 : 5.0, few ? 2.0 : 3.0);
-  return {s, (blocks + s - 1) / s * rows};
 }
 
 size_t part_bytes(int64_t n, int splits, int H) {
@@ -780,7 +756,7 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   const Division div = divide(n, H, topk);
   const size_t need = part_bytes(n, div.splits, H);
   if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return DSA_ERR_WORKSPACE;
-  if (static_cast<int64_t>(n) * div.splits * 2 > INT32_MAX) return DSA_ERR_SHAPE;
+  if (static_cast<int64_t>(n) * div.splits * (kHeads / 16) > INT32_MAX) return DSA_ERR_SHAPE;
   int *err = device_error_word();
   if (!err) return DSA_ERR_CUDA;
 
@@ -799,6 +775,8 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   P.topk = topk;
   P.splits = div.splits;
   P.split_len = div.split_len;
+  P.group_heads = div.group_heads;
+  P.groups = div.group_heads ? (H + div.group_heads - 1) / div.group_heads : 1;
   P.num_kv_rows = num_kv_rows;
   P.cache_rows = num_cache_rows;
   P.num_q_rows = num_q_rows;
@@ -807,18 +785,7 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   P.err = err;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  st = H <= kInt4FewHeads ? launch_attn_int4_few(q, n, P, s) : launch_pairs(q, n, P, s);
+  st = div.group_heads ? launch_attn_int4_few(q, n, P, s) : launch_pairs(q, n, P, s);
   if (st != DSA_OK || div.splits == 1) return st;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(n), static_cast<unsigned>(H));
-  cfg.blockDim = dim3(128);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_join_kernel, P);
-  if (e != cudaSuccess) return cuda_fail(e);
-  return check_launch();
+  return launch_attn_int4_join(n, P, s);
 }

@@ -9,7 +9,6 @@ namespace dsa {
 
 constexpr int kInt4D = 576, kInt4Dv = 512;
 constexpr int kInt4MaxHeads = 128;
-constexpr int kInt4FewHeads = 32;   // up to here sparse_attn_int4_few.cu
 constexpr int kInt4MaxSplits = 32;
 
 struct AttnInt4Params {
@@ -23,14 +22,18 @@ struct AttnInt4Params {
   float2 *part_ml;         // [n * splits][H][2]: (m, l) of each half of the value columns (splits > 1)
   float scale_log2;        // softmax_scale * log2(e)
   int32_t H, topk, splits, split_len;  // split_len: entries per split, a multiple of the kernel's block
+  int32_t groups, group_heads;         // of sparse_attn_int4_few.cu: groups of 16 or 32 heads
   int32_t num_kv_rows, cache_rows, num_q_rows;
   Int4Geom g;
   int *err;
 };
 
-// Launch of the kernel for up to kInt4FewHeads heads (n * splits CTAs).
+// Launch of the kernel for groups of few heads (n * splits * groups CTAs).
 dsa_status launch_attn_int4_few(const void *q, int32_t n, const AttnInt4Params &P, cudaStream_t stream);
 constexpr int kInt4FewRows = 128;   // its entries per block
+
+// Launch of the kernel that joins the parts of P.splits > 1 splits.
+dsa_status launch_attn_int4_join(int32_t n, const AttnInt4Params &P, cudaStream_t stream);
 
 __device__ __forceinline__ float ex2(float x) {
   float y;

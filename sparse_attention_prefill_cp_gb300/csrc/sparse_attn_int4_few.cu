@@ -1,8 +1,9 @@
-// MLA sparse attention over the 4-bit latent-KV cache for up to 32 heads (a
-// tensor-parallel rank's share; what it computes: sparse_attn_int4.cu).
+// MLA sparse attention over the 4-bit latent-KV cache in groups of up to 32
+// heads: a tensor-parallel rank's share, or where a few queries of many heads
+// would leave SMs idle (what it computes: sparse_attn_int4.cu).
 //
-// One CTA takes one query and one split of its entries, in blocks of 128 rows,
-// D = 576, Dv = 512.  Both products run transposed, rows as the M = 128 side of
+// One CTA takes one query, one group of heads and one split of the entries, in
+// blocks of 128 rows, D = 576, Dv = 512.  Both products run transposed, rows as the M = 128 side of
 // the MMA and heads as N = 16 or 32:
 //   S^T [128 rows x heads]    = K [rows x 576] (K-major A) * Q^T
 //   O^T [128 values x heads] += V^T (the same tiles, MN-major A) * P^T,  four times
@@ -134,7 +135,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   int32_t *failed = misc + 1, *bad = misc + 2, *last_used = misc + 4;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int unit = static_cast<int>(blockIdx.x);  // query * splits + split
+  const int unit = static_cast<int>(blockIdx.x) / P.groups;  // query * splits + split
+  const int h0 = (static_cast<int>(blockIdx.x) - unit * P.groups) * HP;
+  const int heads = min(HP, P.H - h0);
   const int query = unit / P.splits;
   const int k0 = (unit - query * P.splits) * P.split_len;
   const int k1 = min(P.topk, k0 + P.split_len);
@@ -154,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tma_prefetch_desc(&q_map);
       mbar_arrive_expect_tx(q_full, kQChunks * HP * 128);
       for (int c = 0; c < kQChunks; ++c)
-        tma_load_3d(smem + C::kOffQ + c * HP * 128, &q_map, 64 * c, 0, qrow, q_full);
+        tma_load_3d(smem + C::kOffQ + c * HP * 128, &q_map, 64 * c, h0, qrow, q_full);
     }
   }
   if (tid == 0) {
@@ -250,14 +253,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
   const int nb = (last + kRows - 1) / kRows;
-  const int64_t part = static_cast<int64_t>(unit) * P.H;  // of the workspace arrays
-  __nv_bfloat16 *out = P.out + static_cast<int64_t>(qrow) * P.H * kDv;
+  const int64_t part = static_cast<int64_t>(unit) * P.H + h0;  // of the workspace arrays
+  __nv_bfloat16 *out = P.out + (static_cast<int64_t>(qrow) * P.H + h0) * kDv;
 
   if (nb == 0) {
     if (P.splits > 1) {
-      if (tid < 2 * P.H) P.part_ml[2 * part + tid] = make_float2(-__builtin_huge_valf(), 0.f);
+      if (tid < 2 * heads) P.part_ml[2 * part + tid] = make_float2(-__builtin_huge_valf(), 0.f);
     } else if (qrow >= 0) {
-      for (int u = tid; u < P.H * (kDv / 8); u += kThreads)
+      for (int u = tid; u < heads * (kDv / 8); u += kThreads)
         *reinterpret_cast<uint4 *>(out + 8 * u) = make_uint4(0u, 0u, 0u, 0u);
     }
     if (q_issued) wait_for(q_full, 0, failed, 60);  // the Q load issued at the start has landed
@@ -542,9 +545,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane < HP) {
         float sum = (red[h] + red[HP + h]) + (red[2 * HP + h] + red[3 * HP + h]);
         if (P.splits > 1) {
-          if (warp < 2 && h < P.H) P.part_ml[2 * (part + h) + warp] = make_float2(m, sum);
+          if (warp < 2 && h < heads) P.part_ml[2 * (part + h) + warp] = make_float2(m, sum);
         } else {
-          if (P.sink && h < P.H) sum += ex2(P.sink[h] * 1.4426950408889634f - m);
+          if (P.sink && h < heads) sum += ex2(P.sink[h0 + h] * 1.4426950408889634f - m);
           inv[h] = sum == 0.f ? 0.f : 1.f / sum;
         }
       }
@@ -570,8 +573,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       softmax_or(false);
       if (tid == 0) {
-        if (P.splits > 1) bulk_store(P.part_o + part * kDv, stage, static_cast<uint32_t>(P.H) * kDv * 4);
-        else bulk_store(out, stage, static_cast<uint32_t>(P.H) * kDv * 2);
+        if (P.splits > 1) bulk_store(P.part_o + part * kDv, stage, static_cast<uint32_t>(heads) * kDv * 4);
+        else bulk_store(out, stage, static_cast<uint32_t>(heads) * kDv * 2);
         bulk_commit();
         bulk_wait_read0();
       }
@@ -600,14 +603,14 @@ dsa_status launch(const void *q, int32_t n, const AttnInt4Params &P, cudaStream_
       cudaFuncSetAttribute(sparse_attn_int4_few_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e);
   sparse_attn_int4_few_kernel<C>
-      <<<static_cast<unsigned>(n) * P.splits, kThreads, C::kSmemBytes, stream>>>(q_map, P);
+      <<<static_cast<unsigned>(n) * P.splits * P.groups, kThreads, C::kSmemBytes, stream>>>(q_map, P);
   return check_launch();
 }
 
 }  // namespace
 
 dsa_status launch_attn_int4_few(const void *q, int32_t n, const AttnInt4Params &P, cudaStream_t stream) {
-  return P.H <= 16 ? launch<FewCfg<16>>(q, n, P, stream) : launch<FewCfg<32>>(q, n, P, stream);
+  return P.group_heads == 16 ? launch<FewCfg<16>>(q, n, P, stream) : launch<FewCfg<32>>(q, n, P, stream);
 }
 
 }  // namespace dsa

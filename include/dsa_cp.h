@@ -607,7 +607,7 @@ dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t t
  *              negative one leaves out as it is; distinct but for those.  NULL:
  *              r = i (then n <= num_q_rows).  Rows of out that none names keep
  *              their values.
- *   topk_idx   int32 [n][topk], any topk >= 1: a negative entry is unused,
+ *   topk_idx   int32 [n][topk], topk 1..2^30: a negative entry is unused,
  *              wherever it stands; a row may be named twice and then counts
  *              twice; a query without a used entry gets zeros
  *   slots      int32 [num_kv_rows]: entry e names cache row slots[e] (negative:
@@ -620,9 +620,10 @@ dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t t
  * beyond num_cache_rows and a q_row at or beyond num_q_rows are
  * DSA_ERR_DEVICE_BOUNDS, and unused.  Only D = 576, Dv = 512 and 1 <= H <= 128
  * are compiled (DSA_ERR_UNSUPPORTED otherwise).  softmax_scale > 0 and finite.
- * bf16 products with fp32 sums; softmax in fp32; the two halves of q.k are
- * exchanged in fp16 (partial sums beyond 65504 saturate).  Few queries are
- * split over their entries, and the parts joined in a fixed order: the same
+ * num_cache_rows >= 1.  bf16 products with fp32 sums, softmax in fp32; many
+ * heads share a query's work between two SMs, which exchange their halves of
+ * q.k in fp16 (11 bits; halves beyond 65504 saturate).  Few queries are split
+ * over their entries and heads, and the parts joined in a fixed order: the same
  * inputs give the same bits.
  */
 dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, const int32_t *q_rows, int32_t n,

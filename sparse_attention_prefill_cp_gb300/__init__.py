@@ -87,6 +87,11 @@ class CPLocalMetadata:
         check(load().dsa_cp_metadata_bind(_ptr(self.buffer), batch, num_tokens, cp_size, C.byref(self.struct)),
               "dsa_cp_metadata_bind")
 
+    @property
+    def token_pos(self) -> torch.Tensor:
+        """local_token_pos: the flat query row of every local slot, -1 = pad (device int32, the buffer's own)."""
+        return self.buffer[self.buffer.numel() - self.tokens_per_rank:]
+
     def to_host(self) -> dict:
         """Read the view back (synchronises); lists trimmed to their valid length."""
         b = self.buffer.cpu().tolist()

@@ -51,6 +51,7 @@ constexpr int kStages = 4;
 constexpr int kNMain = 4;            // 64-wide latent chunks per CTA (128B swizzle), plus one of 32 (64B swizzle)
 constexpr int kDvc = 256;            // value columns per CTA
 constexpr int kThreads = 448;
+constexpr int kMaxTopk = 1 << 30;    // positions in an index row, and a few blocks behind it, are 32-bit
 constexpr int kFirstGatherWarp = 10;
 constexpr int kQMain = kNMain * 128 * 128, kQTail = 128 * 64;
 constexpr int kStageMain = kNMain * kBN * 128, kStageBytes = kStageMain + kBN * 64;
@@ -221,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (__ldg(idx_row + k) >= 0) last = k + 1 - k0;
   last = static_cast<int>(__reduce_max_sync(0xffffffffu, static_cast<unsigned>(last)));
   if (lane == 0) last_used[warp] = last;
+  __syncwarp();
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -734,7 +736,7 @@ using namespace dsa;
 
 extern "C" dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t topk, size_t *bytes) {
   if (!bytes) return DSA_ERR_INVALID_ARG;
-  if (n < 0 || topk < 1) return DSA_ERR_SHAPE;
+  if (n < 0 || topk < 1 || topk > kMaxTopk) return DSA_ERR_SHAPE;
   if (H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
   *bytes = n == 0 ? 0 : part_bytes(n, divide(n, H, topk).splits, H);
   return DSA_OK;
@@ -747,7 +749,8 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
                                              int32_t Dv, void *out, void *workspace, size_t ws_bytes,
                                              dsa_stream_t stream) {
   if (!(softmax_scale > 0.f) || softmax_scale > 3.4e38f) return DSA_ERR_INVALID_ARG;
-  if (n < 0 || num_q_rows < 0 || num_cache_rows < 1 || num_kv_rows < 0 || topk < 1) return DSA_ERR_SHAPE;
+  if (n < 0 || num_q_rows < 0 || num_cache_rows < 1 || num_kv_rows < 0 || topk < 1 || topk > kMaxTopk)
+    return DSA_ERR_SHAPE;
   if (!q_rows && n > num_q_rows) return DSA_ERR_SHAPE;
   if (D != kD || Dv != kDv || H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
   if (n == 0 || num_q_rows == 0) return DSA_OK;

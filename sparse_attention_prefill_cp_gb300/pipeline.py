@@ -214,7 +214,7 @@ class DSAPrefill:
             # a view's pad slots have no entries: zero rows in the view layout, no row in the flat one
             flat = self.fused
             dsa_sparse_attn_int4kv(self._q if flat else self.q_split[r], kv, self.topk_idx[r], self.scale, self.Dv,
-                                   sink, self._kv_slots, self.md[r].buffer[-self.tpr:] if flat else None,
+                                   sink, self._kv_slots, self.md[r].token_pos if flat else None,
                                    self.out if flat else self.out_split[r], stream=st)
         elif self.fused:
             dsa_sparse_attn_prefill_flat(self.md[r], self._q, kv, self.topk_idx[r], self.scale, self.Dv, self.out,

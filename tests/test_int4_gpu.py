@@ -505,7 +505,7 @@ def test_prefill_pipeline_over_the_cache(wl, mode):
             pipe = DSAPrefill(*args, kv_int4=True, kv_int4_direct=True, fused=fused, view_streams=2)
             got = pipe.run(x["q"], kv, x["q_idx"], x["k_idx"], x["w"], x["sink"], kv_slots=sl)
             for r in range(wl.cp_size):
-                pos = pipe.md[r].buffer[-pipe.tpr:].long()
+                pos = pipe.md[r].token_pos.long()
                 use = pos >= 0
                 ref, tol = attend_ref(x["q"][pos[use]], rows.double(), pipe.topk_idx[r][use], wl.scale, x["sink"])
                 assert ((got[pos[use]].double() - ref).abs() <= tol).all()

@@ -744,8 +744,8 @@ def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: to
             raise ValueError(f"attn_sink must be [{H}]")
     if slots is not None:
         _need(slots, torch.int32, "slots")
-        if slots.dim() != 1:
-            raise ValueError("slots must be [num_kv_rows]")
+        if slots.dim() != 1 or (n and not slots.numel()):   # an empty one has no address, which means: no slots
+            raise ValueError("slots must be [num_kv_rows], with a row at least")
     if q_rows is None:
         if n != m:
             raise ValueError("q and topk_idx must have the same number of rows (or pass q_rows)")

@@ -435,6 +435,80 @@ def test_streams_and_graphs():
     dsa.dsa_poll_device_error()
 
 
+def test_empty_slots_are_refused():
+    """Slots without a row name none; they are not the call without slots."""
+    cache, _ = make_cache(8, 40)
+    q = torch.zeros(2, 16, D, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(2, 4, dtype=torch.int32, device="cuda")
+    none = torch.empty(0, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV, slots=none)
+    assert dsa.dsa_sparse_attn_int4kv(q[:0], cache, idx[:0], SCALE, DV, slots=none).shape == (0, 16, DV)
+
+
+@pytest.mark.parametrize("n,H,topk", [(1, 100, 2048), (2, 64, 700), (1, 33, 64), (2, 128, 129), (1, 17, 9000),
+                                      (1, 49, 4097), (2, 127, 2048)])
+def test_a_query_or_two_of_many_heads(n, H, topk):
+    """The division over groups of heads, the last of them partial, with a sink, slots and holes."""
+    R, KV = 5000, 4000
+    cache, rows = make_cache(R, 41)
+    g = torch.Generator().manual_seed(42 + H)
+    slots = torch.randperm(R, generator=g)[:KV].to(torch.int32)
+    slots[::97] = -1
+    idx = draw_idx(n, topk, KV, 43, "scattered")
+    q = torch.randn(n, H, D, generator=g).to(torch.bfloat16).cuda()
+    sink = torch.randn(H, generator=g).cuda()
+    got = dsa.dsa_sparse_attn_int4kv(q, cache, idx.cuda(), SCALE, DV, attn_sink=sink, slots=slots.cuda())
+    dsa.dsa_poll_device_error()
+    ref, tol = attend_ref(q, rows, idx.cuda(), SCALE, sink, slots.cuda())
+    assert ((got.double() - ref).abs() <= tol).all()
+
+
+def test_two_streams_at_once():
+    """Calls of different divisions on two streams, each with the workspace of its own stream."""
+    cache, _ = make_cache(3000, 44)
+    g = torch.Generator().manual_seed(45)
+    calls = []
+    for n, H, topk in ((3, 128, 2048), (5, 16, 2048), (90, 128, 300), (1, 64, 2048)):
+        q = torch.randn(n, H, D, generator=g).to(torch.bfloat16).cuda()
+        idx = draw_idx(n, topk, 3000, n, "scattered").cuda()
+        calls.append((q, idx, dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(8):
+        for k, st in enumerate(streams):
+            for q, idx, _want in calls if k == 0 else calls[::-1]:
+                got[k].append(dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV, stream=st))
+    torch.cuda.synchronize()
+    for k in range(2):
+        order = calls if k == 0 else calls[::-1]
+        for i, out in enumerate(got[k]):
+            assert torch.equal(out, order[i % len(calls)][2])
+    dsa.dsa_poll_device_error()
+
+
+@pytest.mark.parametrize("n,H,topk", [(200, 128, 130), (160, 16, 300), (1, 128, 2048), (6, 32, 2048)])
+def test_replays_of_every_division(n, H, topk):
+    """A captured call replayed over changed inputs: pairs and groups, one pass and split with a join."""
+    cache, _ = make_cache(2500, 46)
+    g = torch.Generator().manual_seed(47)
+    q = torch.randn(n, H, D, generator=g).to(torch.bfloat16).cuda()
+    idx = draw_idx(n, topk, 2500, 48, "tail").cuda()
+    dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV)
+    for seed in (49, 50):
+        q.copy_(torch.randn(n, H, D, generator=torch.Generator().manual_seed(seed)))
+        idx.copy_(draw_idx(n, topk, 2500, seed, "scattered"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(held, dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV))
+    dsa.dsa_poll_device_error()
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("page", [64, 16])

@@ -52,6 +52,7 @@ constexpr int kNMain = 4;            // 64-wide latent chunks per CTA (128B swiz
 constexpr int kDvc = 256;            // value columns per CTA
 constexpr int kThreads = 448;
 constexpr int kMaxTopk = 1 << 30;    // positions in an index row, and a few blocks behind it, are 32-bit
+constexpr int kOrderedTopk = 1024;   // lists from this length on are taken longest first (divide)
 constexpr int kFirstGatherWarp = 10;
 constexpr int kQMain = kNMain * 128 * 128, kQTail = 128 * 64;
 constexpr int kStageMain = kNMain * kBN * 128, kStageBytes = kStageMain + kBN * 64;
@@ -126,8 +127,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t crank = cluster_ctarank(), peer = crank ^ 1u;
   const int unit = static_cast<int>(blockIdx.x >> 1);  // query * splits + split
-  const int query = unit / P.splits;
+  int query = unit / P.splits;
   const int k0 = (unit - query * P.splits) * P.split_len;
+  if (P.order) {  // splits == 1
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the order is still being made
+    query = P.order[unit];
+  }
   const int k1 = min(P.topk, k0 + P.split_len);
   const int main_dim0 = static_cast<int>(crank) * kDvc;
   const int tail_dim0 = kDv + 32 * static_cast<int>(crank);
@@ -636,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w == 0 && wait_for(o_staged, 0, failed, 76) && ok && h < P.H) {
         bulk_store(P.part_o + (part + h) * kDv + main_dim0, ost + h * kPartRow, kDvc * 4);
         bulk_commit();
-        bulk_wait_read0();
+        bulk_wait_done();
       }
     }
   }
@@ -663,8 +668,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 // heads: 64 queries 60 us, against 150 in groups); groups win up to 32 heads
 // (16 heads: 37 against 60) and for a query or two of many heads, whose splits
 // alone do not fill the SMs.
+//
+// Two to four waves of pairs over long lists take the queries in the order of
+// their lists' lengths (sparse_attn_int4_order.cu; one more load before a pair
+// can start, and a small launch).  us for 2048 entries and 128 heads, lengths
+// log-uniform to 3000 / all lists full, in the order given -> longest first:
+//   152 queries  74.7 -> 61.8 / 117 -> 121     256  104 -> 77 / 232 -> 238
+// One wave and a half gains what it costs (100 queries 65.9 -> 60.7 / 112 ->
+// 117), as do lists of 512; of many waves the last matters little (1000
+// queries: 289 -> 287 / 804 -> 832), and groups of 16 heads pay more for the
+// load (400 queries 86 -> 68 / 180 -> 191).
 struct Division {
   int splits, split_len, group_heads;  // group_heads 0: pairs
+  bool ordered;                        // by the length of the queries' lists
 };
 
 Division divide(int64_t n, int H, int topk) {
@@ -674,7 +690,7 @@ Division divide(int64_t n, int H, int topk) {
   };
   const Way ways[3] = {{0, kBN, 9.0, 1.5}, {16, kInt4FewRows, 4.0, 3.7}, {32, kInt4FewRows, 4.5, 4.1}};
   const int sms = num_sms();
-  Division best{1, 0, 0};
+  Division best{1, 0, 0, false};
   double best_cost = 1e300;
   for (const Way &w : ways) {
     const int blocks = (topk + w.rows - 1) / w.rows;
@@ -688,15 +704,18 @@ Division divide(int64_t n, int H, int topk) {
       const double cost = waves * (w.fixed + w.block * per) + (s > 1 ? 3.0 + parts : 0.0);
       if (cost < best_cost) {
         best_cost = cost;
-        best = {s, per * w.rows, w.group_heads};
+        const bool ordered = !w.group_heads && s == 1 && n >= 2 * units && n <= 4 * units && n <= kInt4MaxOrdered &&
+                             topk >= kOrderedTopk;
+        best = {s, per * w.rows, w.group_heads, ordered};
       }
     }
   }
   return best;
 }
 
-size_t part_bytes(int64_t n, int splits, int H) {
-  return splits > 1 ? static_cast<size_t>(n) * splits * H * (kDv * 4 + 16) : 0;
+size_t workspace_bytes(int64_t n, const Division &d, int H) {
+  if (d.ordered) return static_cast<size_t>(n) * 4;
+  return d.splits > 1 ? static_cast<size_t>(n) * d.splits * H * (kDv * 4 + 16) : 0;
 }
 
 dsa_status launch_pairs(const void *q, int32_t n, const AttnInt4Params &P, cudaStream_t stream) {
@@ -717,13 +736,15 @@ dsa_status launch_pairs(const void *q, int32_t n, const AttnInt4Params &P, cudaS
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kSmemBytes;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = P.order ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, sparse_attn_int4_kernel, qmain, qtail, P);
   if (e != cudaSuccess) return cuda_fail(e);
   return check_launch();
@@ -738,7 +759,7 @@ extern "C" dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H
   if (!bytes) return DSA_ERR_INVALID_ARG;
   if (n < 0 || topk < 1 || topk > kMaxTopk) return DSA_ERR_SHAPE;
   if (H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
-  *bytes = n == 0 ? 0 : part_bytes(n, divide(n, H, topk).splits, H);
+  *bytes = n == 0 ? 0 : workspace_bytes(n, divide(n, H, topk), H);
   return DSA_OK;
 }
 
@@ -757,7 +778,7 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   if (!q || !kv_cache || !topk_idx || !out) return DSA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
   const Division div = divide(n, H, topk);
-  const size_t need = part_bytes(n, div.splits, H);
+  const size_t need = workspace_bytes(n, div, H);
   if (need > 0 && (!workspace || !aligned16(workspace) || ws_bytes < need)) return DSA_ERR_WORKSPACE;
   if (static_cast<int64_t>(n) * div.splits * (kHeads / 16) > INT32_MAX) return DSA_ERR_SHAPE;
   int *err = device_error_word();
@@ -788,6 +809,12 @@ extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, 
   P.err = err;
 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (div.ordered) {
+    int32_t *order = static_cast<int32_t *>(workspace);
+    st = launch_attn_int4_order(n, P, order, s);
+    if (st != DSA_OK) return st;
+    P.order = order;
+  }
   st = div.group_heads ? launch_attn_int4_few(q, n, P, s) : launch_pairs(q, n, P, s);
   if (st != DSA_OK || div.splits == 1) return st;
   return launch_attn_int4_join(n, P, s);

@@ -10,6 +10,7 @@ namespace dsa {
 constexpr int kInt4D = 576, kInt4Dv = 512;
 constexpr int kInt4MaxHeads = 128;
 constexpr int kInt4MaxSplits = 32;
+constexpr int kInt4MaxOrdered = 1024;  // queries that are started in order of their lists' lengths
 
 struct AttnInt4Params {
   const uint8_t *cache;    // [cache_rows][row_bytes]
@@ -17,6 +18,7 @@ struct AttnInt4Params {
   const int32_t *idx;      // [n][topk]
   const int32_t *q_rows;   // [n] row of q and out (negative: none), or nullptr: row i
   const float *sink;       // [H] or nullptr
+  const int32_t *order;    // [n] the query that a pair takes as its i-th, or nullptr: i (splits == 1)
   __nv_bfloat16 *out;      // [num_q_rows][H][Dv]
   float *part_o;           // [n * splits][H][Dv] (splits > 1)
   float2 *part_ml;         // [n * splits][H][2]: (m, l) of each half of the value columns (splits > 1)
@@ -31,6 +33,10 @@ struct AttnInt4Params {
 // Launch of the kernel for groups of few heads (n * splits * groups CTAs).
 dsa_status launch_attn_int4_few(const void *q, int32_t n, const AttnInt4Params &P, cudaStream_t stream);
 constexpr int kInt4FewRows = 128;   // its entries per block
+
+// Launch of the kernel that fills P.order; what is launched next may start
+// while it runs.
+dsa_status launch_attn_int4_order(int32_t n, const AttnInt4Params &P, int32_t *order, cudaStream_t stream);
 
 // Launch of the kernel that joins the parts of P.splits > 1 splits.
 dsa_status launch_attn_int4_join(int32_t n, const AttnInt4Params &P, cudaStream_t stream);
@@ -118,5 +124,9 @@ __device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t 
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                : "memory");
 }
+
+// Until this thread's bulk copies are complete, not only read: the join of the
+// parts may be resident before this kernel has ended.
+__device__ __forceinline__ void bulk_wait_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 }  // namespace dsa

@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (P.splits > 1) bulk_store(P.part_o + part * kDv, stage, static_cast<uint32_t>(heads) * kDv * 4);
         else bulk_store(out, stage, static_cast<uint32_t>(heads) * kDv * 2);
         bulk_commit();
-        bulk_wait_read0();
+        bulk_wait_done();
       }
     }
   }

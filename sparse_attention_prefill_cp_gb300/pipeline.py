@@ -158,7 +158,7 @@ class DSAPrefill:
         """Kernel launches of one ``run``: metadata per view, 3 splits (2
         fused), the cache's dequantisation (if any), per view (indexer + top-k)
         per workspace chunk and one attention (two where the attention over the
-        4-bit cache is split), 1 rerange (0 fused)."""
+        4-bit cache is split or orders its queries), 1 rerange (0 fused)."""
         ld = (self.max_kv_len + 3) // 4 * 4
         tile = 8 if self.HI == 64 else 128
         rows_fit = (self.workspace.numel() // (ld * 4)) // tile * tile
@@ -167,8 +167,8 @@ class DSAPrefill:
         md = self.cp_size * (2 if self.window and self.compress_ratio > 1 else 1)
         swa = self.cp_size if self.window else 0
         dequant = int(self.kv_rows is not None)
-        joins = int(self.kv_int4_direct and dsa_sparse_attn_int4kv_workspace_size(self.tpr, self.H, self.topk) > 0)
-        return md + splits + dequant + self.cp_size * (2 * chunks + 1 + joins) + swa + reranges
+        second = int(self.kv_int4_direct and dsa_sparse_attn_int4kv_workspace_size(self.tpr, self.H, self.topk) > 0)
+        return md + splits + dequant + self.cp_size * (2 * chunks + 1 + second) + swa + reranges
 
     def metadata(self, stream=None):                                     # a1
         for r in range(self.cp_size):

@@ -509,6 +509,55 @@ def test_replays_of_every_division(n, H, topk):
     dsa.dsa_poll_device_error()
 
 
+@pytest.mark.parametrize("n,H", [(152, 128), (181, 70), (304, 40), (305, 40)])
+def test_ragged_lists_of_many_queries(n, H):
+    """Two to four waves of long lists are taken longest first: lists of every length, empty and head-masked ones, rows
+    without a query, and replays over other lengths, where the order has to be made anew."""
+    R, m, topk = 3000, n + 3, 1100
+    cache, rows = make_cache(R, 51)
+    g = torch.Generator().manual_seed(52)
+
+    def lists():
+        idx = torch.randint(0, R, (n, topk), generator=g).to(torch.int32)
+        lens = torch.exp(torch.rand(n, generator=g) * 7.2).long().clamp(max=topk)
+        lens[:2] = torch.tensor([0, topk])
+        idx[torch.arange(topk)[None] >= lens[:, None]] = -1
+        idx[5, : topk - 3], idx[5, topk - 3 :] = -1, 7
+        return idx.cuda()
+
+    q_rows = torch.randperm(m, generator=g)[:n].to(torch.int32)
+    q_rows[9] = -1
+    q_rows = q_rows.cuda()
+    q = torch.randn(m, H, D, generator=g).to(torch.bfloat16).cuda()
+    out = torch.full((m, H, DV), 3.0, dtype=torch.bfloat16, device="cuda")
+    idx = lists()
+
+    def run():
+        return dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV, q_rows=q_rows, out=out)
+
+    def check():
+        torch.cuda.synchronize()
+        use = q_rows >= 0
+        at = q_rows[use].long()
+        ref, tol = attend_ref(q[at], rows, idx[use], SCALE)
+        assert ((out[at].double() - ref).abs() <= tol).all()
+        rest = torch.ones(m, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert (out[rest] == 3.0).all()
+
+    run()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for _ in range(2):
+        idx.copy_(lists())
+        out.fill_(3.0)
+        graph.replay()
+        check()
+    dsa.dsa_poll_device_error()
+
+
 # ------------------------------------------------------------------ together
 
 @pytest.mark.parametrize("page", [64, 16])

@@ -591,7 +591,9 @@ dsa_status dsa_kv_int4_dequantize(const void *cache, int32_t num_cache_rows, int
                                   const int32_t *rows, int32_t num_rows, void *kv, dsa_stream_t stream);
 
 /* Host only (the current device's SM count enters).  Workspace bytes of
- * dsa_sparse_attn_int4kv for n queries, 0 where it needs none. */
+ * dsa_sparse_attn_int4kv for n queries, 0 where it needs none (parts of queries
+ * whose entries are split, or the order in which many are taken).  Calls that
+ * may run at the same time need a workspace each. */
 dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t topk, size_t *bytes);
 
 /*

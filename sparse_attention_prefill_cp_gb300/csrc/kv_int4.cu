@@ -7,8 +7,8 @@
 //   c   = clamp(rint(x / (s_b * 2^e)), -7, 7)   (s_b = 0: c = 0)
 // so the row's power of two gives the range (any bf16 magnitude up to 2^125)
 // and the block's E4M3 the precision.  Symmetric integers, not E2M1: at 16
-// columns a block their uniform step, max|x_b| / 7, has a third less squared
-// error than E2M1's on normal values, and they decode with one fma a pair.
+// columns a block their uniform step, max|x_b| / 7, has 18 % less squared error
+// than E2M1 scaled to max|x_b| / 6 on normal values, and they decode with one fma a pair.
 //
 // Decisions are those of the exact quotients, although quotients are products
 // with an approximate reciprocal: for x = X 2^i (X of 8 bits) and s = S 2^j (S

@@ -37,6 +37,12 @@
 // clusters, which leave unnormalised fp32 O halves and (m, l) per head in the
 // workspace; a second kernel joins them in split order (no atomics, so the
 // result does not depend on timing).
+//
+// What bounds it: the softmax warps' chain (S out of tensor memory, exchange,
+// maximum, exponentials, P), about 2,950 cycles a block of 64 entries against
+// 1,100 of MMA work.  76 queries of 128 heads x 2048 entries: 60 us, 724
+// TFLOP/s; 64 queries 59 us; 2048 queries 1.51 ms, 772 TFLOP/s (0.41 of the
+// measured bf16 rate), tensor pipe active 30 % of the time, DRAM 17 %.
 #include "sparse_attn_int4.cuh"
 #include "internal.h"
 
@@ -664,10 +670,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   a wave of 16-head CTAs 4 + 3.7 per block of 128
 //   a wave of 32-head CTAs 4.5 + 4.1 per block of 128
 //   joining splits         3 + the parts written and read at 5 TB/s
-// Pairs win where there are many heads and enough queries for the SMs (128
-// heads: 64 queries 60 us, against 150 in groups); groups win up to 32 heads
-// (16 heads: 37 against 60) and for a query or two of many heads, whose splits
-// alone do not fill the SMs.
+// Measured with each way forced (pairs / groups of 16 / of 32, us, rows in L2):
+//   128 heads,  1 query   14.5 /  11.5 /  12.9    128 heads, 64 queries  57.5 / 228 / 120
+//    32 heads, 64 queries 55.0 /  54.1 /  38.3     16 heads, 64 queries  54.6 /  33 /  35
+// Pairs win where there are many heads and enough queries for the SMs, groups up
+// to 32 heads, and for a query or two of many heads, whose splits alone do not
+// fill the SMs.
 //
 // Two to four waves of pairs over long lists take the queries in the order of
 // their lists' lengths (sparse_attn_int4_order.cu; one more load before a pair

@@ -34,6 +34,11 @@
 // four warps decides, and only where a logit is above (and in the first block)
 // are the block's maxima reduced and O^T and the sums rescaled.  P is rounded
 // to bf16 (2^-9) for the MMA; logits, exponentials' sums and O are fp32.
+//
+// What bounds it: the chain of a block of 128 rows, about 6,400 cycles, half of
+// them decoding; the tensor pipe is active 7 % of the time, DRAM 26 %.  152
+// queries of 16 heads x 2048 entries: 64 us, 2.2 TB/s of cache bytes; 64
+// queries 38 us; 4 queries, 16 parts each and their join, 11 us.
 #include "sparse_attn_int4.cuh"
 #include "internal.h"
 

@@ -594,8 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     uint8_t *ost = smem + kOffStage;  // free: every PV is done
     if (P.splits == 1) {
-      if (P.sink && h < P.H) l += ex2(P.sink[h] * 1.4426950408889634f - m_used);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      // entries that all lead to no row leave l = 0 and m = -inf: zeros, whatever the sink (its power would be
+      // e^(-inf + inf) for a sink of -inf); a NaN among the logits is a NaN in l
+      const bool none = l == 0.f;
+      if (P.sink && h < P.H && !none) l += ex2(P.sink[h] * 1.4426950408889634f - m_used);
+      const float inv = none ? 0.f : 1.f / l;
       // normalised rows through shared memory, 16-byte unit u of row h at
       // u ^ (h & 31), so that neither the row-wise writes nor the reads
       // collide; then each warp stores whole 512-byte rows

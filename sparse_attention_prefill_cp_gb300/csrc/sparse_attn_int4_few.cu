@@ -552,8 +552,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (P.splits > 1) {
           if (warp < 2 && h < heads) P.part_ml[2 * (part + h) + warp] = make_float2(m, sum);
         } else {
-          if (P.sink && h < heads) sum += ex2(P.sink[h0 + h] * 1.4426950408889634f - m);
-          inv[h] = sum == 0.f ? 0.f : 1.f / sum;
+          // entries that all lead to no row leave sum = 0 and m = -inf: zeros, whatever the sink
+          const bool empty = sum == 0.f;
+          if (P.sink && h < heads && !empty) sum += ex2(P.sink[h0 + h] * 1.4426950408889634f - m);
+          inv[h] = empty ? 0.f : 1.f / sum;
         }
       }
       __syncwarp();

@@ -1,0 +1,148 @@
+"""The attention over the 4-bit cache in every division of a call (pairs of
+SMs, groups of 16 and of 32 heads, each with and without splits of the
+entries), where its answer must not depend on the division.
+
+Tolerance, elementwise, from the roundings.  With p_j the exact weights:
+  the result to bf16:                          2^-8 of it
+  each P to bf16 for the product:              2^-8 p_j |v_j|
+  a logit off by d_j, in the weight itself and in the denominator:
+                                               expm1(d_j) p_j (|v_j| + |out|)
+  exp2 and fp32 sums of up to 2048 terms:      2^-14 p_j |v_j|
+and 2^-6 of the sum of these for their products.  d_j: q.k is summed in fp32,
+36 steps of an MMA that each round 16 products and the sum so far, aligned to
+the largest of the 17, below 2^-24 of it: 36 * 17 * 2^-24 < 2^-14.7 of
+sum_d |q_d k_d| at the very worst.  Where q and k are integers whose sums stay
+below 2^24, q.k is exact and d_j is what the scale and the exponent's fma
+round, 2^-21 of the largest logit.
+"""
+import pytest
+import torch
+
+import sparse_attention_prefill_cp_gb300 as dsa
+
+D, DV, SCALE = 576, 512, 192 ** -0.5
+INF = float("inf")
+
+# n, H, topk of a call in every division on 152 SMs
+DIVISIONS = {"pairs": (90, 128, 130), "pairs, split": (8, 128, 2048), "pairs, longest first": (152, 128, 1100),
+             "groups of 16": (160, 16, 300), "groups of 16, split": (1, 16, 2048),
+             "groups of 32": (160, 32, 300), "groups of 32, split": (6, 32, 2048)}
+every_division = pytest.mark.parametrize("n,H,topk", DIVISIONS.values(), ids=DIVISIONS.keys())
+
+
+@pytest.fixture(autouse=True)
+def _gpu(request):
+    if request.node.get_closest_marker("gpu") is None:
+        yield
+        return
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    yield
+    dsa.dsa_poll_device_error()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def latent(n, seed):
+    return torch.randn(n, D, generator=gen(seed)).to(torch.bfloat16)
+
+
+def store(kv):
+    """(cache, the values it stands for in 64 bits)."""
+    cache = dsa.dsa_kv_int4_quantize(kv.cuda(), DV)
+    return cache, dsa.dsa_kv_int4_dequantize(cache, D, DV).double()
+
+
+def attend64(q, rows, idx, sink=None, slots=None, exact_sums=False):
+    """(out, tolerance) of the attention in 64 bits, a query at a time."""
+    q, rows, idx = q.cuda().double(), rows.cuda(), idx.cuda()
+    n, H = q.shape[:2]
+    out = torch.zeros(n, H, DV, dtype=torch.float64, device="cuda")
+    tol = torch.zeros_like(out)
+    for i in range(n):
+        pick = idx[i].long()
+        pick = pick[pick >= 0]
+        if slots is not None:
+            pick = slots[pick].long()
+            pick = pick[pick >= 0]
+        if not pick.numel():
+            continue
+        k = rows[pick]
+        l = SCALE * (q[i] @ k.T)
+        m = l.amax(1, keepdim=True)
+        p = torch.exp(l - m)
+        den = p.sum(1, keepdim=True)
+        if sink is not None:
+            den = den + torch.exp(sink.double()[:, None] - m)
+        p = p / den
+        out[i] = p @ k[:, :DV]
+        if exact_sums:
+            d = 2.0 ** -21 * l.abs().amax(1, keepdim=True).expand_as(l)
+        else:
+            d = SCALE * 2.0 ** -14.7 * (q[i].abs() @ k.abs().T)
+        off = p * torch.expm1(d)
+        v = k[:, :DV].abs()
+        t = 2.0 ** -8 * out[i].abs() + (p * (2.0 ** -8 + 2.0 ** -14) + off) @ v + out[i].abs() * off.sum(1, keepdim=True)
+        tol[i] = t * (1 + 2.0 ** -6) + 1e-30
+    return out, tol
+
+
+def check(got, ref, tol):
+    off = (got.double() - ref).abs()
+    assert (off <= tol).all(), (off / tol).nan_to_num(nan=INF).max().item()
+    # the roundings are independent: their norm stays well below the sum of their bounds
+    norm = ref.norm()
+    assert norm == 0 or (got.double() - ref).norm() / norm <= 1e-2
+
+
+# ------------------------------------------------------------------ queries without a row
+
+@pytest.mark.gpu
+@every_division
+def test_entries_that_lead_to_no_row_give_zeros(n, H, topk):
+    """Every third query names KV rows whose slot is negative, and nothing else: zeros, whatever the sink.  The last
+    one names a row that holds a NaN beside them: NaN, whatever the sink."""
+    R = 200
+    kv = latent(R, 1)
+    kv[R - 1, 7] = float("nan")
+    cache, rows = store(kv)
+    slots = torch.arange(R, dtype=torch.int32)
+    slots[150:R - 1] = -1
+    idx = torch.randint(0, 150, (n, topk), generator=gen(2)).to(torch.int32)
+    none = [i for i in range(0, n, 3) if i == 0 or i < n - 1]
+    idx[none] = torch.randint(150, R - 1, (len(none), topk), generator=gen(3)).to(torch.int32)
+    if n > 1:
+        idx[n - 1] = 160
+        idx[n - 1, topk // 2] = R - 1
+    use = max(n - 1, 1)
+    q = torch.randn(n, H, D, generator=gen(4)).to(torch.bfloat16).cuda()
+    idx, slots = idx.cuda(), slots.cuda()
+    for level in (None, 2.0, INF, -INF):
+        sink = None if level is None else torch.full((H,), level, device="cuda")
+        got = dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV, attn_sink=sink, slots=slots)
+        assert not got[none].any()                      # a NaN counts as something
+        if n > 1:
+            assert torch.isnan(got[n - 1]).all()
+        ref, tol = attend64(q[:use], rows, idx[:use], sink, slots)
+        check(got[:use], ref, tol)
+
+
+@pytest.mark.gpu
+@every_division
+def test_entries_out_of_range_give_zeros(n, H, topk):
+    """A query whose entries are all out of range has none: reported, and zeros under a sink of -inf."""
+    cache, rows = store(latent(64, 5))
+    idx = torch.randint(0, 64, (n, topk), generator=gen(6)).to(torch.int32)
+    idx[0] = 64
+    q = torch.randn(n, H, D, generator=gen(7)).to(torch.bfloat16).cuda()
+    sink = torch.full((H,), -INF, device="cuda")
+    got = dsa.dsa_sparse_attn_int4kv(q, cache, idx.cuda(), SCALE, DV, attn_sink=sink)
+    with pytest.raises(dsa.DSAError) as err:
+        dsa.dsa_poll_device_error()
+    assert err.value.status == 7 and err.value.detail[0] == 50
+    idx[0] = -1
+    ref, tol = attend64(q, rows, idx, sink)
+    check(got, ref, tol)
+    assert not got[0].any()

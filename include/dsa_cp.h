@@ -622,11 +622,10 @@ dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t t
  * beyond num_cache_rows and a q_row at or beyond num_q_rows are
  * DSA_ERR_DEVICE_BOUNDS, and unused.  Only D = 576, Dv = 512 and 1 <= H <= 128
  * are compiled (DSA_ERR_UNSUPPORTED otherwise).  softmax_scale > 0 and finite.
- * num_cache_rows >= 1.  bf16 products with fp32 sums, softmax in fp32; many
- * heads share a query's work between two SMs, which exchange their halves of
- * q.k in fp16 (11 bits; halves beyond 65504 saturate).  Few queries are split
- * over their entries and heads, and the parts joined in a fixed order: the same
- * inputs give the same bits.
+ * num_cache_rows >= 1.  bf16 products with fp32 sums, softmax in fp32 but for
+ * the weights that multiply the values (bf16, each within 2^-8 of itself).  Few
+ * queries are split over their entries and heads, and the parts joined in a
+ * fixed order: the same inputs give the same bits.
  */
 dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, const int32_t *q_rows, int32_t n,
                                   const void *kv_cache, int32_t num_cache_rows, const int32_t *slots,
@@ -647,7 +646,7 @@ dsa_status dsa_poll_device_error(dsa_stream_t stream);
  * slot, top-k overflow, attention slot, attention index, metadata), 47-51
  * bounds checks around the 4-bit cache (written slot, row read back, index
  * entry, its cache row, query row; the detail is the position in the list),
- * 60-76 waits of the attention over it (the detail is the key block). */
+ * 60-79 waits of the attention over it (the detail is the key block). */
 dsa_status dsa_poll_device_error_detail(dsa_stream_t stream, int32_t *detail);
 
 /* Static string for a status code. */

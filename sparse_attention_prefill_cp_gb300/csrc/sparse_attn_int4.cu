@@ -11,22 +11,26 @@
 // memory, so CTA c owns value columns [256c, 256c + 256) and computes the
 // partial QK over latent dims [256c, 256c + 256) + [512 + 32c, 512 + 32c + 32):
 // each CTA decodes its half of a row once, and one shared-memory tile serves
-// as QK's K-major B and PV's MN-major B.  The pair exchanges partial S tiles
-// through distributed shared memory, in fp16: a bulk copy of 16 KB each way
-// and block is what the links carry in a block's time (13.6 B/clk measured,
-// 32 KB of fp32 would take 2,400 cycles of it); the rounding is 2^-12 of a
-// partial sum of q.k, a few 1e-4 in the logit for logits of unit size, and
-// below the 2^-9 of P's bf16.  P is bf16 for the MMA; statistics, sums and O
-// are fp32.  A partial sum beyond 65504 saturates there.
+// as QK's K-major B and PV's MN-major B.  CTA c does the softmax of heads
+// [64c, 64c + 64): it gets its peer's partial S of them, in fp32 (16 KB a block
+// of 64 entries), and returns their P and the factor by which the head's O is
+// to be rescaled (8.25 KB), so that both halves of a result come from one
+// softmax over sums held in 32 bits.  (Exchanging whole partial S tiles in fp32
+// and doing every softmax twice took 36 % longer on 2,048 queries: 32 KB each
+// way at the link's 13.6 B/clk are 2,400 cycles of a block's time.)  P is bf16
+// for the MMA, each entry within 2^-8 of itself; statistics, sums and O are
+// fp32.
 //
 // Tensor memory (512 columns): O (256), two S buffers (2 x 64), the CTA's 256
-// main Q dims as bf16 (128).  14 warps: 0-7 softmax in two warpgroups (one
+// main Q dims as bf16 (128).  15 warps: 0-7 softmax in two warpgroups (one
 // head row = one TMEM lane per thread; warpgroup w owns columns [32w, 32w + 32)
-// of every block of 64 entries), 8 TMA for Q then MMA issue, 9 the exchange
-// agent, 10-13 the gather.  Nothing in the roles' loops is a call (a failed
-// wait or a bad index is noted and recorded at the end): a call's register
-// conventions made the softmax spill, and the gather's loads drove the spilled
-// values out of the small L1 that 227 KB of shared memory leave.
+// of every block of 64 entries; of a warpgroup's four warps two have heads of
+// this CTA, two heads of the peer, for which they send S and rescale O), 8 TMA
+// for Q then MMA issue, 9 and 14 the copies to the peer, 10-13 the gather.
+// Nothing in the roles' loops is a call (a failed wait or a bad index is noted
+// and recorded at the end): a call's register conventions made the softmax
+// spill, and the gather's loads drove the spilled values out of the small L1
+// that 227 KB of shared memory leave.
 //
 // The gather reads a row's codes, scales and exponent, decodes to bf16 with
 // one shift, one LOP3 and one packed fma per two values (no conversion
@@ -38,11 +42,12 @@
 // workspace; a second kernel joins them in split order (no atomics, so the
 // result does not depend on timing).
 //
-// What bounds it: the softmax warps' chain (S out of tensor memory, exchange,
-// maximum, exponentials, P), about 2,950 cycles a block of 64 entries against
-// 1,100 of MMA work.  76 queries of 128 heads x 2048 entries: 60 us, 724
-// TFLOP/s; 64 queries 59 us; 2048 queries 1.51 ms, 772 TFLOP/s (0.41 of the
-// measured bf16 rate), tensor pipe active 30 % of the time, DRAM 17 %.
+// What bounds it: the way of a block from a freed stage to the next, decoding
+// (about 1,900 cycles), QK, partial S to the peer, softmax, P to the peer, PV,
+// about 12,000 cycles over four stages: a block of 64 entries every 3,000
+// cycles, 1,100 of them MMA work.  76 queries of 128 heads x 2048 entries:
+// 64 us, 680 TFLOP/s; 64 queries 63 us; 2048 queries 1.52 ms, 770 TFLOP/s (0.40
+// of the measured bf16 rate).
 #include "sparse_attn_int4.cuh"
 #include "internal.h"
 
@@ -56,33 +61,69 @@ constexpr int kHalf = kBN / 2;       // columns per softmax warpgroup
 constexpr int kStages = 4;
 constexpr int kNMain = 4;            // 64-wide latent chunks per CTA (128B swizzle), plus one of 32 (64B swizzle)
 constexpr int kDvc = 256;            // value columns per CTA
-constexpr int kThreads = 448;
+constexpr int kThreads = 480;
 constexpr int kMaxTopk = 1 << 30;    // positions in an index row, and a few blocks behind it, are 32-bit
 constexpr int kOrderedTopk = 1024;   // lists from this length on are taken longest first (divide)
-constexpr int kFirstGatherWarp = 10;
+constexpr int kFirstGatherWarp = 10, kPAgentWarp = 14;
 constexpr int kQMain = kNMain * 128 * 128, kQTail = 128 * 64;
 constexpr int kStageMain = kNMain * kBN * 128, kStageBytes = kStageMain + kBN * 64;
 constexpr int kQKMainSteps = kNMain * 4, kQKSteps = kQKMainSteps + 2, kPVSteps = kBN / 16;
 constexpr int kSCol = kDvc, kQCol = kSCol + 2 * kBN, kTmemCols = 512;
-constexpr int kRecvBytes = 128 * kBN * 2;  // one partial-S tile (fp16), rows swizzled; P (bf16) overwrites it
+// A P tile (bf16, 64 entries a row): per CTA its heads' rows, and beside them their rescaling factors, so that one
+// copy takes both to the peer: factors of CTA 0, rows of CTA 0, rows of CTA 1, factors of CTA 1
+constexpr int kPRows = kHeads / 2 * 128, kAlphaBytes = kHeads / 2 * 4, kPMsg = kPRows + kAlphaBytes;
+constexpr int kPBytes = 2 * kPRows + 1024;
+constexpr int kXHalf = kHeads / 2 * kHalf * 4;  // partial S (fp32) of the peer's heads, 32 entries of them
+constexpr int kXBytes = 2 * kXHalf;
 constexpr int kOffStage = 0;
 constexpr int kOffQStage = kOffStage + kStageBytes;  // Q main staged in stages 1..2 at start
 constexpr int kOffQTail = kOffStage + kStages * kStageBytes;
-constexpr int kOffRecv = kOffQTail + kQTail;
-constexpr int kOffStg = kOffRecv + 2 * kRecvBytes;
-constexpr int kOffRed = kOffStg + 2 * kRecvBytes;     // [3][2 warpgroups][128] floats
-constexpr int kOffBar = kOffRed + 3 * 2 * 128 * 4;
-constexpr int kNumBars = 2 + 2 * kStages + 2 * 9 + 2;
-constexpr int kOffMisc = kOffBar + kNumBars * 8;      // [0] tmem, [1] failed wait, [2..3] bad index, [4..19] last used entry per warp, [20..27] masks
+constexpr int kOffP = kOffQTail + kQTail + 1024;  // of the rows
+constexpr int kOffRecv = kOffP + 2 * kPBytes;
+constexpr int kOffStg = kOffRecv + kXBytes;
+constexpr int kOffRed = kOffStg + kXBytes;            // floats: block maxima [2 blocks][2 warpgroups][128],
+constexpr int kSums = 4 * 128, kInv = 6 * 128;        // sums [2 warpgroups][128], 1 / denominator [128]
+constexpr int kOffBar = kOffRed + 7 * 128 * 4;
+constexpr int kNumBars = 2 + 2 * kStages + 2 * 3 + 2 * 3 + 1 + 2 * 6 + 3;
+// [0] tmem, [1] failed wait, [2..3] bad index, [4..18] last used entry per warp, [20..27] masks
+constexpr int kOffMisc = kOffBar + (kNumBars + 1) / 2 * 16;
 constexpr int kSmemBytes = kOffMisc + 28 * 4 + 1024;
 constexpr uint32_t kIdescQK = idesc_bf16(128, kBN, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16(128, kDvc, false, true);
 static_assert(kQCol + kNMain * 32 <= kTmemCols, "TMEM budget");
 static_assert(kQMain <= 2 * kStageBytes, "Q staging fits in stages 1..2");
-static_assert(kStageBytes % 1024 == 0 && kOffQTail % 1024 == 0 && kOffRecv % 1024 == 0, "alignment");
+static_assert(kStageBytes % 1024 == 0 && kPBytes % 1024 == 0 && kOffQTail % 1024 == 0 && kOffP % 1024 == 0 &&
+                  kOffRecv % 1024 == 0,
+              "alignment");
 constexpr int kPartRow = kDvc * 4 + 16;
 static_assert(kHeads * kPartRow <= kStages * kStageBytes, "the fp32 O half fits in the stages");
 static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
+
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
+  float4 r;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+
+// mbar_test for what the peer's copies complete.
+__device__ __forceinline__ bool mbar_test_cluster(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// A float into the peer's shared memory.
+__device__ __forceinline__ void st_cluster_f32(uint32_t raddr, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(raddr), "f"(x) : "memory");
+}
 
 __device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
   __syncwarp();
@@ -116,15 +157,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *kv_empty = kv_full + kStages;   // [kStages] PV done with the stage (MMA commit)
   uint64_t *s_full = kv_empty + kStages;    // [2] QK done (MMA commit)
   uint64_t *s_free = s_full + 2;            // [2] S read out of TMEM (8 softmax warps)
-  uint64_t *p_full = s_free + 2;            // [2] P tile written (8 softmax warps)
-  uint64_t *pv_done = p_full + 2;           // [2] PV done, its P tile free (MMA commit)
-  uint64_t *recv_full = pv_done + 2;        // [2] the peer's partial S landed (bulk copy)
-  uint64_t *recv_empty = recv_full + 2;     // [2] the peer is done with what we sent (peer's agent)
-  uint64_t *red_full = recv_empty + 2;      // [2] both warpgroups' block maxima written (8 warps)
-  uint64_t *staged = red_full + 2;          // [2] our partial-S tile written (8 softmax warps)
-  uint64_t *stg_free = staged + 2;          // [2] the bulk copy has read our tile (sender)
-  uint64_t *fin_full = stg_free + 2;        // both warpgroups' denominators written (8 warps)
-  uint64_t *o_staged = fin_full + 1;        // O rows staged in smem (8 warps)
+  uint64_t *red_full = s_free + 2;          // [2] both warpgroups' block maxima written (4 warps)
+  uint64_t *recv_full = red_full + 2;       // [2] the peer's partial S of our heads landed, a half (bulk copy)
+  uint64_t *staged = recv_full + 2;         // [2] partial S of the peer's heads written, a half (2 warps)
+  uint64_t *stg_free = staged + 2;          // [2] the bulk copy has read that half (sender)
+  uint64_t *recv_empty = stg_free + 2;      // the peer has read what we sent (one of its threads)
+  uint64_t *p_own = recv_empty + 1;         // [2] P of our heads written (4 warps)
+  uint64_t *p_sent = p_own + 2;             // [2] the bulk copy has read it (sender)
+  uint64_t *p_msg = p_sent + 2;             // [2] P and the rescaling factors of the peer's heads landed (bulk copies)
+  uint64_t *o_ready = p_msg + 2;            // [2] O is rescaled for P (8 softmax warps)
+  uint64_t *p_empty = o_ready + 2;          // [2] the peer's PV has read the P that we sent (one of its threads)
+  uint64_t *pv_done = p_empty + 2;          // [2] PV done, its P tile free (MMA commit)
+  uint64_t *sum_full = pv_done + 2;         // both warpgroups' denominators written (4 warps)
+  uint64_t *inv_full = sum_full + 1;        // 1 / denominator of all heads written (2 warps of either CTA)
+  uint64_t *o_staged = inv_full + 1;        // O rows staged in smem (8 warps)
   int32_t *misc = reinterpret_cast<int32_t *>(smem + kOffMisc);
   int32_t *last_used = misc + 4;
   uint16_t *masks = reinterpret_cast<uint16_t *>(misc + 20);  // [kStages][4]: bit r of half-word w = row 16w + r is used
@@ -172,15 +218,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int b = 0; b < 2; ++b) {
       mbar_init(&s_full[b], 1);
       mbar_init(&s_free[b], 8);
-      mbar_init(&p_full[b], 8);
-      mbar_init(&pv_done[b], 1);
+      mbar_init(&red_full[b], 4);
       mbar_init(&recv_full[b], 1);
-      mbar_init(&recv_empty[b], 1);
-      mbar_init(&red_full[b], 8);
-      mbar_init(&staged[b], 8);
+      mbar_init(&staged[b], 2);
       mbar_init(&stg_free[b], 1);
+      mbar_init(&p_own[b], 4);
+      mbar_init(&p_sent[b], 1);
+      mbar_init(&p_msg[b], 1);
+      mbar_init(&o_ready[b], 8);
+      mbar_init(&p_empty[b], 1);
+      mbar_init(&pv_done[b], 1);
     }
-    mbar_init(fin_full, 8);
+    mbar_init(recv_empty, 1);
+    mbar_init(sum_full, 4);
+    mbar_init(inv_full, 4);
     mbar_init(o_staged, 8);
     fence_mbar_init();
   }
@@ -211,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     ld_once_u8(exponent, P.cache + static_cast<int64_t>(max(rr, 0)) * P.g.row_bytes + P.g.exponent, rr >= 0);
   };
   int32_t early_bad[2] = {0, 0};  // an index out of range, before shared memory is set up
-  if (warp >= kFirstGatherWarp) {
+  if (warp >= kFirstGatherWarp && warp < kPAgentWarp) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       code[q] = make_uint4(0u, 0u, 0u, 0u);
@@ -258,17 +309,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (q_issued) wait_for(q_full, 0, failed, 60);  // the Q load issued at the start has landed
   } else if (warp == 8) {
     // ---------------- MMA issuer, event-driven: QK(j) as soon as its rows are
-    // there, its S buffer is free and PV(j - 3) has been issued, PV(i) as soon as
-    // P(i) is written; each stream in order.  The whole warp runs the loop and
-    // one elected lane issues: descriptors and addresses then live in uniform
-    // registers (the least an MMA takes is 45 cycles so; 63 from a branch of one
-    // lane).
+    // there and its S buffer is free, PV(i) as soon as both CTAs' rows of P(i) are
+    // there and O is rescaled for it; each stream in order.  The whole warp runs
+    // the loop and one elected lane issues: descriptors and addresses then live
+    // in uniform registers (alone on the SM, with a commit after every eight, an
+    // MMA of N = 64 takes 48 cycles so; 59 from a branch of one lane).
     const bool issuer = elect_one();
     const uint32_t st_addr = smem_u32(smem + kOffStage);
     const uint64_t qk_b0 = smem_desc(st_addr, 16, 1024, kLayoutSW128);
     const uint64_t qk_t0 = smem_desc(st_addr + kStageMain, 16, 512, kLayoutSW64);
     const uint64_t qt_a0 = smem_desc(smem_u32(smem + kOffQTail), 16, 512, kLayoutSW64);
-    const uint64_t pv_a0 = smem_desc(smem_u32(smem + kOffRecv), 16, 1024, kLayoutSW128);
+    const uint64_t pv_a0 = smem_desc(smem_u32(smem + kOffP), 16, 1024, kLayoutSW128);
     const uint64_t pv_b0 = smem_desc(st_addr, kBN * 128, 1024, kLayoutSW128);
     const uint32_t s_tm = tmem + kSCol, q_tm = tmem + kQCol;
     bool ok = __all_sync(0xffffffffu, wait_for(q_full, 0, failed, 61) && wait_for(q_ready, 0, failed, 61));
@@ -277,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     long long t_prog = clock64();
     while (ok && pv < nb) {
       bool progressed = false;
-      if (qk < nb && qk < pv + 3 &&
+      if (qk < nb &&
           __all_sync(0xffffffffu, mbar_test(&kv_full[qk % kStages], (qk / kStages) & 1) &&
                                       (qk < 2 || mbar_test(&s_free[qk & 1], ((qk - 2) >> 1) & 1)))) {
         tc_fence_after();
@@ -301,11 +352,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++qk;
         progressed = true;
       }
-      if (pv < qk && __all_sync(0xffffffffu, mbar_test(&p_full[pv & 1], (pv >> 1) & 1))) {
+      if (pv < qk && __all_sync(0xffffffffu, mbar_test(&p_own[pv & 1], (pv >> 1) & 1) &&
+                                                     mbar_test(&o_ready[pv & 1], (pv >> 1) & 1) &&
+                                                     mbar_test(&p_msg[pv & 1], (pv >> 1) & 1))) {
         tc_fence_after();
         const int bi = pv & 1, si = pv % kStages;
+        const uint64_t pb = desc_add(pv_a0, static_cast<uint32_t>(bi * kPBytes) >> 4);
         const uint64_t vb = desc_add(pv_b0, static_cast<uint32_t>(si * kStageBytes) >> 4);
-        const uint64_t pb = desc_add(pv_a0, static_cast<uint32_t>(bi * kRecvBytes) >> 4);
         if (issuer) {
 #pragma unroll
           for (int k = 0; k < kPVSteps; ++k)
@@ -327,29 +380,42 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     if (lane == 0) {
-      // ---------------- exchange agent: ships each staged partial-S tile to the
-      // peer with one bulk copy, and tells the peer when its tiles have been read
+      // ---------------- sends the partial S of the peer's heads
       const uint32_t peer_recv = map_to_cta(smem_u32(smem + kOffRecv), peer);
       const uint32_t peer_full = map_to_cta(smem_u32(recv_full), peer);
       bool ok = true;
-      for (int t = 0; ok && t <= nb; ++t) {
-        if (t < nb) {
-          const int b = t & 1;
-          if (!(ok = wait_for(&staged[b], (t >> 1) & 1, failed, 63, t))) break;
-          if (t >= 2 && !(ok = wait_for<true>(&recv_empty[b], ((t >> 1) & 1) ^ 1, failed, 64, t))) break;
-          bulk_copy_to_peer(peer_recv + b * kRecvBytes, smem + kOffStg + b * kRecvBytes, kRecvBytes, peer_full + b * 8);
+      for (int t = 0; ok && t < nb; ++t) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          ok = ok && wait_for(&staged[w], t & 1, failed, 63, t);
+          if (w == 0 && t >= 1) ok = ok && wait_for<true>(recv_empty, (t - 1) & 1, failed, 64, t);
+          if (!ok) break;
+          bulk_copy_to_peer(peer_recv + w * kXHalf, smem + kOffStg + w * kXHalf, kXHalf, peer_full + 8 * w);
           bulk_commit();
-          bulk_wait_read0();
-          mbar_arrive(&stg_free[b]);
         }
-        if (t >= 1) {
-          const int b = (t - 1) & 1;
-          // PV(t-1) has read P(t-1), which sits in the tile the peer filled
-          if (!(ok = wait_for(&pv_done[b], ((t - 1) >> 1) & 1, failed, 65, t - 1))) break;
-          mbar_arrive_remote_relaxed(&recv_empty[b], peer);
-        }
+        if (!ok) break;
+        bulk_wait_read<1>();
+        mbar_arrive(&stg_free[0]);
+        bulk_wait_read0();
+        mbar_arrive(&stg_free[1]);
       }
-      bulk_wait_read0();
+      bulk_wait_done();  // after a failed wait a copy may still be under way
+    }
+  } else if (warp == kPAgentWarp) {
+    if (lane == 0) {
+      // ---------------- sends P and the rescaling factors of our heads; to the same place in the peer's P tile
+      uint8_t *msg = smem + kOffP - kAlphaBytes + crank * kPMsg;
+      const uint32_t peer_msg = map_to_cta(smem_u32(msg), peer), peer_full = map_to_cta(smem_u32(p_msg), peer);
+      for (int t = 0; t < nb; ++t) {
+        const int b = t & 1;
+        if (!wait_for(&p_own[b], (t >> 1) & 1, failed, 65, t)) break;
+        if (t >= 2 && !wait_for<true>(&p_empty[b], ((t >> 1) & 1) ^ 1, failed, 77, t)) break;
+        bulk_copy_to_peer(peer_msg + b * kPBytes, msg + b * kPBytes, kPMsg, peer_full + 8 * b);
+        bulk_commit();
+        bulk_wait_read0();
+        mbar_arrive(&p_sent[b]);
+      }
+      bulk_wait_done();
     }
   } else if (warp >= kFirstGatherWarp) {
     if (early_bad[0]) {
@@ -425,7 +491,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ---------------- softmax: two warpgroups; thread = head row h = TMEM lane,
     // warpgroup w owns columns [32w, 32w + 32) of every block.  Every decision
-    // that guards a tcgen05.ld/st (.sync.aligned) is made warp-uniform.
+    // that guards a tcgen05.ld/st (.sync.aligned) is made warp-uniform.  A warp's
+    // heads are either this CTA's or the peer's (TMEM lanes belong to a warp's
+    // rank in its warpgroup).
     const int h = tid & 127, w = tid >> 7;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     bool ok = __all_sync(0xffffffffu, wait_for(q_full, 0, failed, 68, -1));
@@ -450,23 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     warp_arrive(q_ready, lane);
 
-    uint8_t *recv0 = smem + kOffRecv;
-    // our 32 columns of a partial S row, rounded to fp16, for the exchange agent
-    auto stage = [&](int j, const float (&x)[32]) {
-      uint8_t *rowp = smem + kOffStg + (j & 1) * kRecvBytes + h * 128;
-#pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        const int u = (w * kHalf + k) >> 3;
-        *reinterpret_cast<uint4 *>(rowp + ((u ^ (h & 7)) << 4)) =
-            make_uint4(pack_f16x2_sat(x[k], x[k + 1]), pack_f16x2_sat(x[k + 2], x[k + 3]),
-                       pack_f16x2_sat(x[k + 4], x[k + 5]), pack_f16x2_sat(x[k + 6], x[k + 7]));
-      }
-      fence_proxy_async_smem();  // the bulk copy reads the tile through the async proxy
-      warp_arrive(&staged[j & 1], lane);
-    };
-    // our 32 columns of S(j), raw q.k; the buffer is then free for QK(j+2)
-    const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
-    auto load_s = [&](int j, float (&x)[32]) {
+    const bool ours = (warp & 3) >> 1 == static_cast<int>(crank);
+    // our row and half of an exchange tile, less the tile's offset: a row of 128 bytes, unit u at u ^ (h & 7)
+    const uint32_t x_row = smem_u32(smem) + w * kXHalf + (h & 63) * 128 + ((h & 7) << 4);
+    const uint32_t p_row = smem_u32(smem) + h * 128 + ((h & 7) << 4);  // of the P tile
+    uint8_t *my_alpha = smem + kOffP + (h < 64 ? -kAlphaBytes : 2 * kPRows) + 4 * (h & 63);
+    // our 32 columns of S(j), raw q.k over this CTA's dims; the buffer is then free for QK(j+2)
+    auto take_s = [&](int j, float (&x)[32]) {
       uint32_t r[32];
       tmem_ld32(lane_base + kSCol + (j & 1) * kBN + w * kHalf, r);
       tmem_ld_wait();
@@ -475,51 +533,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       warp_arrive(&s_free[j & 1], lane);
     };
-
-    float m_used = -__builtin_huge_valf(), l = 0.f;  // m in log2 units; l over this warpgroup's columns
-    float s_a[32], s_b[32];
-    if (ok) {
-      ok = __all_sync(0xffffffffu, wait_for(&s_full[0], 0, failed, 69, 0));
-      if (ok) {
-        tc_fence_after();
-        load_s(0, s_a);
-        stage(0, s_a);
+    if (!ours) {
+      // ---- heads of the peer, event-driven: their partial S(js) goes to the peer
+      // as soon as it is there and the last one has left; P(jp) and the rescaling
+      // factors come back; PV(je) frees its P tile for the peer's next but one.
+      const bool first = w == 0 && (h & 63) == 0;  // one thread
+      if (first)
+        for (int j = 0; j < 2; ++j) mbar_arrive_expect_tx(&p_msg[j], kPMsg);
+      int js = 0, jp = 0, je = 0;
+      long long t_prog = clock64();
+      while (ok && jp < nb) {
+        bool progressed = false;
+        if (js < nb && __all_sync(0xffffffffu, mbar_test(&s_full[js & 1], (js >> 1) & 1) &&
+                                                   (js == 0 || mbar_test(&stg_free[w], (js - 1) & 1)))) {
+          float x[32];
+          tc_fence_after();
+          take_s(js, x);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            st_shared_v4((x_row + kOffStg) ^ (u << 4), __float_as_uint(x[4 * u]), __float_as_uint(x[4 * u + 1]),
+                         __float_as_uint(x[4 * u + 2]), __float_as_uint(x[4 * u + 3]));
+          fence_proxy_async_smem();  // the bulk copy reads the tile through the async proxy
+          warp_arrive(&staged[w], lane);
+          ++js;
+          progressed = true;
+        }
+        if (je + 2 < nb && __all_sync(0xffffffffu, mbar_test(&pv_done[je & 1], (je >> 1) & 1))) {
+          if (first) mbar_arrive_remote_relaxed(&p_empty[je & 1], peer);
+          ++je;
+          progressed = true;
+        }
+        if (__all_sync(0xffffffffu, mbar_test_cluster(&p_msg[jp & 1], (jp >> 1) & 1))) {
+          const int b = jp & 1;
+          const float alpha = *reinterpret_cast<const float *>(my_alpha + b * kPBytes);
+          if (first && jp + 2 < nb) mbar_arrive_expect_tx(&p_msg[b], kPMsg);
+          if (jp >= 1 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            ok = __all_sync(0xffffffffu, wait_for(&pv_done[b ^ 1], ((jp - 1) >> 1) & 1, failed, 73, jp));
+            if (!ok) break;
+            tc_fence_after();
+            scale_o(lane_base, w * (kDvc / 2), (w + 1) * (kDvc / 2), alpha);
+            tc_fence_before();
+          }
+          warp_arrive(&o_ready[b], lane);
+          ++jp;
+          progressed = true;
+        }
+        const long long now = clock64();
+        if (progressed) {
+          t_prog = now;
+        } else if (__any_sync(0xffffffffu, now - t_prog > kWaitLimitCycles)) {
+          *failed = 78 << 24 | (jp & 0xffffff);
+          ok = false;
+        }
       }
     }
-    auto block = [&](int i, float (&x)[32], float (&nxt)[32]) -> bool {
-      const int b = i & 1;
-      if (i + 1 < nb) {
-        // fetch and ship block i+1 ahead: the peer has it by the time it starts block i+1
-        const int b1 = (i + 1) & 1;
-        const bool tile_free = i < 1 || mbar_try_wait_hint(&stg_free[b1], ((i - 1) >> 1) & 1);
-        ok = wait_for(&s_full[b1], ((i + 1) >> 1) & 1, failed, 69, i + 1);
-        if (!tile_free) ok = ok && wait_for(&stg_free[b1], ((i - 1) >> 1) & 1, failed, 70, i + 1);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return false;
-        tc_fence_after();
-        load_s(i + 1, nxt);
-        stage(i + 1, nxt);
-      }
-      if (tid == 0) mbar_arrive_expect_tx(&recv_full[b], kRecvBytes);
-      // the block's rows were complete before its QK; their barrier too orders the mask word read below, and is
-      // asked first, its answer's latency hidden behind the other's
+    const uint64_t sc2 = f2_pack(P.scale_log2, P.scale_log2);
+    float m_used = -__builtin_huge_valf(), l = 0.f;  // m in log2 units; l over this warpgroup's columns
+    // ---- a head of ours
+    auto block = [&](int i, const int b) -> bool {
+      if ((h & 63) == 0) mbar_arrive_expect_tx(&recv_full[w], kXHalf);
+      // the block's rows were complete before its QK, too; their barrier orders the mask word read below
       const bool rows_full = mbar_try_wait_hint(&kv_full[i % kStages], (i / kStages) & 1);
-      ok = wait_for<true>(&recv_full[b], (i >> 1) & 1, failed, 71, i);
+      ok = wait_for(&s_full[b], (i >> 1) & 1, failed, 69, i) && wait_for<true>(&recv_full[w], i & 1, failed, 71, i);
       if (!rows_full) ok = ok && wait_for(&kv_full[i % kStages], (i / kStages) & 1, failed, 71, i);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return false;
-      const uint8_t *my_recv = recv0 + b * kRecvBytes + h * 128;
+      tc_fence_after();
+      float x[32];
+      take_s(i, x);
 #pragma unroll
-      for (int k = 0; k < 32; k += 8) {
-        const int u = (w * kHalf + k) >> 3;
-        const uint4 t = *reinterpret_cast<const uint4 *>(my_recv + ((u ^ (h & 7)) << 4));
-        const uint32_t pv[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float lo, hi;
-          unpack_f16x2(pv[e], lo, hi);
-          f2_unpack(f2_add(f2_pack(x[k + 2 * e], x[k + 2 * e + 1]), f2_pack(lo, hi)), x[k + 2 * e], x[k + 2 * e + 1]);
-        }
+      for (int u = 0; u < 8; ++u) {
+        const float4 t = ld_shared_v4((x_row + kOffRecv) ^ (u << 4));
+        f2_unpack(f2_add(f2_pack(x[4 * u], x[4 * u + 1]), f2_pack(t.x, t.y)), x[4 * u], x[4 * u + 1]);
+        f2_unpack(f2_add(f2_pack(x[4 * u + 2], x[4 * u + 3]), f2_pack(t.z, t.w)), x[4 * u + 2], x[4 * u + 3]);
       }
       const uint32_t used = reinterpret_cast<const uint32_t *>(masks)[2 * (i % kStages) + w];
       if (used != 0xffffffffu) {
@@ -534,22 +620,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                       fmaxf(x[8 * q + 6], x[8 * q + 7]));
       red[(b * 2 + w) * 128 + h] = fmaxf(fmax3(m3[0], m3[1], m3[2]), m3[3]);
       warp_arrive(&red_full[b], lane);
+      // PV(i-2) and the copy to the peer have read P(i-2)?
+      const uint32_t before = ((i >> 1) & 1) ^ 1;  // parity of block i-2
+      const bool p_free =
+          __all_sync(0xffffffffu, i < 2 || (mbar_test(&pv_done[b], before) && mbar_test(&p_sent[b], before)));
       ok = __all_sync(0xffffffffu, wait_for(&red_full[b], (i >> 1) & 1, failed, 72, i));
       if (!ok) return false;
+      if (w == 0 && (h & 63) == 0) mbar_arrive_remote_relaxed(recv_empty, peer);  // all four warps have read it
       const float mblk = fmaxf(red[(b * 2) * 128 + h], red[(b * 2 + 1) * 128 + h]) * P.scale_log2;  // log2 units
       // lazy rescale: only when some row of the warp saw its max grow by more
       // than 2^8.  Both warpgroups see the same row maxima, so they decide alike.
-      if (__any_sync(0xffffffffu, mblk > m_used + 8.f)) {
+      float alpha = 1.f;
+      const bool moved = __any_sync(0xffffffffu, mblk > m_used + 8.f);
+      if (moved) {
         const float m_new = fmaxf(m_used, mblk);
-        const float alpha = m_new > m_used ? ex2(m_used - m_new) : 1.f;  // both -inf: nothing yet
-        if (i >= 1) {
-          // O holds PV(i-1): rescale this warpgroup's half of it before PV(i) accumulates
-          ok = __all_sync(0xffffffffu, wait_for(&pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1, failed, 73, i));
-          if (!ok) return false;
-          tc_fence_after();
-          scale_o(lane_base, w * (kDvc / 2), (w + 1) * (kDvc / 2), alpha);
-          tc_fence_before();
-        }
+        if (m_new > m_used) alpha = ex2(m_used - m_new);  // else both may be -inf: nothing yet
         l *= alpha;
         m_used = m_new;
       }
@@ -570,35 +655,59 @@ __global__ void __launch_bounds__(kThreads, 1)
       f2_unpack(acc[0], s0, s1);
       f2_unpack(acc[1], s2, s3);
       l += (s0 + s1) + (s2 + s3);
-      uint8_t *prow = recv0 + b * kRecvBytes + h * 128;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int uu = w * 4 + u;
-        *reinterpret_cast<uint4 *>(prow + ((uu ^ (h & 7)) << 4)) =
-            make_uint4(packed[4 * u], packed[4 * u + 1], packed[4 * u + 2], packed[4 * u + 3]);
+      if (!p_free) {
+        ok = __all_sync(0xffffffffu, wait_for(&pv_done[b], before, failed, 73, i) &&
+                                         wait_for(&p_sent[b], before, failed, 79, i));
+        if (!ok) return false;
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        st_shared_v4((p_row + kOffP + b * kPBytes) ^ ((w * 4 + u) << 4), packed[4 * u], packed[4 * u + 1],
+                     packed[4 * u + 2], packed[4 * u + 3]);
+      if (w == 0) *reinterpret_cast<float *>(my_alpha + b * kPBytes) = alpha;
       fence_proxy_async_smem();
-      warp_arrive(&p_full[b], lane);
+      warp_arrive(&p_own[b], lane);
+      if (moved && i >= 1) {
+        // O holds PV(i-1): rescale this warpgroup's half of it before PV(i) accumulates; P(i) is on its way meanwhile
+        ok = __all_sync(0xffffffffu, wait_for(&pv_done[b ^ 1], ((i - 1) >> 1) & 1, failed, 73, i));
+        if (!ok) return false;
+        tc_fence_after();
+        scale_o(lane_base, w * (kDvc / 2), (w + 1) * (kDvc / 2), alpha);
+        tc_fence_before();
+      }
+      warp_arrive(&o_ready[b], lane);
       return true;
     };
-    for (int i = 0; ok && i < nb; i += 2) {
-      ok = block(i, s_a, s_b);
-      if (ok && i + 1 < nb) ok = block(i + 1, s_b, s_a);
+    if (ours) {
+      for (int i = 0; ok && i < nb; i += 2) {
+        ok = block(i, 0);
+        if (ok && i + 1 < nb) ok = block(i + 1, 1);
+      }
     }
     ok = __all_sync(0xffffffffu, ok && wait_for(&pv_done[(nb - 1) & 1], ((nb - 1) >> 1) & 1, failed, 74, nb));
-    // the two warpgroups' partial sums of the softmax denominator
-    red[(4 + w) * 128 + h] = l;
-    warp_arrive(fin_full, lane);
-    ok = __all_sync(0xffffffffu, wait_for(fin_full, 0, failed, 75) && ok);
-    l = red[4 * 128 + h] + red[5 * 128 + h];
+    if (ours) {
+      // the two warpgroups' partial sums of the softmax denominator
+      red[kSums + w * 128 + h] = l;
+      warp_arrive(sum_full, lane);
+      ok = __all_sync(0xffffffffu, wait_for(sum_full, 0, failed, 75) && ok);
+      l = red[kSums + h] + red[kSums + 128 + h];
+      if (w == 0 && P.splits == 1) {
+        // entries that all lead to no row leave l = 0 and m = -inf: zeros, whatever the sink (its power would be
+        // e^(-inf + inf) for a sink of -inf); a NaN among the logits is a NaN in l
+        const bool none = l == 0.f;
+        if (P.sink && h < P.H && !none) l += ex2(P.sink[h] * 1.4426950408889634f - m_used);
+        const float inv = none ? 0.f : 1.f / l;
+        red[kInv + h] = inv;
+        st_cluster_f32(map_to_cta(smem_u32(red + kInv + h), peer), inv);
+        warp_arrive(inv_full, lane);
+        if (lane == 0) mbar_arrive_remote(inv_full, peer);
+      }
+    }
     tc_fence_after();
     uint8_t *ost = smem + kOffStage;  // free: every PV is done
     if (P.splits == 1) {
-      // entries that all lead to no row leave l = 0 and m = -inf: zeros, whatever the sink (its power would be
-      // e^(-inf + inf) for a sink of -inf); a NaN among the logits is a NaN in l
-      const bool none = l == 0.f;
-      if (P.sink && h < P.H && !none) l += ex2(P.sink[h] * 1.4426950408889634f - m_used);
-      const float inv = none ? 0.f : 1.f / l;
+      ok = __all_sync(0xffffffffu, wait_for<true>(inv_full, 0, failed, 75, 1) && ok);
+      const float inv = red[kInv + h];
       // normalised rows through shared memory, 16-byte unit u of row h at
       // u ^ (h & 31), so that neither the row-wise writes nor the reads
       // collide; then each warp stores whole 512-byte rows
@@ -643,7 +752,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint4 *>(ost + h * kPartRow + (c + k) * 4) =
                 make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
         }
-        if (w == 0 && h < P.H) P.part_ml[2 * (part + h) + crank] = make_float2(m_used, l);
+        if (ours && w == 0 && h < P.H)
+          reinterpret_cast<float4 *>(P.part_ml)[part + h] = make_float4(m_used, l, m_used, l);
       }
       fence_proxy_async_smem();
       warp_arrive(o_staged, lane);
@@ -669,13 +779,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 // single CTAs with groups of 16 or 32 heads (sparse_attn_int4_few.cu), and over
 // splits of a query's entries.  The times below are what the kernels took, in
 // us, for 1 to 256 queries of 2048 entries in 1 to 32 splits, to about 10 %:
-//   a wave of pairs        9 + 1.5 per block of  64 entries (any number of heads)
+//   a wave of pairs       10 + 1.6 per block of  64 entries (any number of heads)
 //   a wave of 16-head CTAs 4 + 3.7 per block of 128
 //   a wave of 32-head CTAs 4.5 + 4.1 per block of 128
 //   joining splits         3 + the parts written and read at 5 TB/s
 // Measured with each way forced (pairs / groups of 16 / of 32, us, rows in L2):
-//   128 heads,  1 query   14.5 /  11.5 /  12.9    128 heads, 64 queries  57.5 / 228 / 120
-//    32 heads, 64 queries 55.0 /  54.1 /  38.3     16 heads, 64 queries  54.6 /  33 /  35
+//   128 heads,  1 query   15.6 /  11.5 /  12.6    128 heads, 64 queries  60.7 / 228 / 120
+//    32 heads, 64 queries 56.8 /  54.1 /  38.4     16 heads, 64 queries  55.9 /  33 /  35
 // Pairs win where there are many heads and enough queries for the SMs, groups up
 // to 32 heads, and for a query or two of many heads, whose splits alone do not
 // fill the SMs.
@@ -684,11 +794,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // their lists' lengths (sparse_attn_int4_order.cu; one more load before a pair
 // can start, and a small launch).  us for 2048 entries and 128 heads, lengths
 // log-uniform to 3000 / all lists full, in the order given -> longest first:
-//   152 queries  74.7 -> 61.8 / 117 -> 121     256  104 -> 77 / 232 -> 238
-// One wave and a half gains what it costs (100 queries 65.9 -> 60.7 / 112 ->
-// 117), as do lists of 512; of many waves the last matters little (1000
-// queries: 289 -> 287 / 804 -> 832), and groups of 16 heads pay more for the
-// load (400 queries 86 -> 68 / 180 -> 191).
+//   152 queries  82.0 -> 65.4 / 126 -> 130     256  114 -> 86 / 248 -> 253
+// One wave and a half gains little more than it costs (100 queries 70.7 -> 63.9
+// / 120 -> 124), lists of 512 the less (200 queries 52.8 -> 50.6 / 72 -> 77); of
+// many waves the last matters little (1000 queries: 318 -> 315 / 858 -> 885),
+// and groups of 16 heads pay more for the load (400 queries 86 -> 68 / 180 ->
+// 191).
 struct Division {
   int splits, split_len, group_heads;  // group_heads 0: pairs
   bool ordered;                        // by the length of the queries' lists
@@ -699,7 +810,7 @@ Division divide(int64_t n, int H, int topk) {
     int group_heads, rows;
     double fixed, block;
   };
-  const Way ways[3] = {{0, kBN, 9.0, 1.5}, {16, kInt4FewRows, 4.0, 3.7}, {32, kInt4FewRows, 4.5, 4.1}};
+  const Way ways[3] = {{0, kBN, 10.0, 1.6}, {16, kInt4FewRows, 4.0, 3.7}, {32, kInt4FewRows, 4.5, 4.1}};
   const int sms = num_sms();
   Division best{1, 0, 0, false};
   double best_cost = 1e300;

@@ -84,7 +84,7 @@ def attend64(q, rows, idx, sink=None, slots=None, exact_sums=False):
             d = SCALE * 2.0 ** -14.7 * (q[i].abs() @ k.abs().T)
         off = p * torch.expm1(d)
         v = k[:, :DV].abs()
-        t = 2.0 ** -8 * out[i].abs() + (p * (2.0 ** -8 + 2.0 ** -14) + off) @ v + out[i].abs() * off.sum(1, keepdim=True)
+        t = (p * (2.0 ** -8 + 2.0 ** -14) + off) @ v + out[i].abs() * (2.0 ** -8 + off.sum(1, keepdim=True))
         tol[i] = t * (1 + 2.0 ** -6) + 1e-30
     return out, tol
 
@@ -146,3 +146,78 @@ def test_entries_out_of_range_give_zeros(n, H, topk):
     ref, tol = attend64(q, rows, idx, sink)
     check(got, ref, tol)
     assert not got[0].any()
+
+
+# ------------------------------------------------------------------ sums of q.k
+
+@pytest.mark.gpu
+@every_division
+@pytest.mark.parametrize("size", [8, 64])
+def test_halves_of_q_k_that_cancel(n, H, topk, size):
+    """q.k whose halves over columns 0-255 and 256-511 are large (some 12,000 with size 8, 99,000 with size 64) and
+    cancel to a few units: integers, exact in 32 bits."""
+    R = 300
+    kv = torch.empty(R, D)
+    sign = torch.where(torch.rand(DV // 2, generator=gen(8)) < 0.5, -1.0, 1.0)
+    kv[:, :256] = 6 * sign
+    kv[:, :256:16] = 7 * sign[::16]
+    kv[:, 256:DV] = kv[:, :256]
+    kv[:, DV:] = 0
+    # a row differs from the others in the rope columns, and in a few values on either side
+    kv[:, DV:] = torch.randint(-2, 3, (R, D - DV), generator=gen(9)).float() / size
+    flip = torch.randint(1, 16, (R, 2), generator=gen(10))
+    for side in range(2):
+        at = 256 * side + 16 * torch.randint(0, 16, (R,), generator=gen(11 + side)) + flip[:, side]
+        kv[torch.arange(R), at] -= sign[at % 256] * torch.randint(0, 3, (R,), generator=gen(13 + side))
+    cache, rows = store(kv.to(torch.bfloat16))
+    assert torch.equal(rows.cpu(), kv.double())
+    q = torch.empty(n, H, D)
+    q[:, :, :256] = size * sign
+    q[:, :, 256:DV] = -size * sign
+    q[:, :, DV:] = torch.randint(-size, size + 1, (n, H, D - DV), generator=gen(15)).float()
+    q = q.to(torch.bfloat16)
+    idx = torch.randint(0, R, (n, topk), generator=gen(16)).to(torch.int32).cuda()
+    s0 = (q[0, 0, :256].double() @ kv[:, :256].double().T).abs()
+    assert s0.min() > 1300 * size                       # 65504 is left behind with size 64
+    got = dsa.dsa_sparse_attn_int4kv(q.cuda(), cache, idx, SCALE, DV)
+    ref, tol = attend64(q, rows, idx, exact_sums=True)
+    check(got, ref, tol)
+
+
+@pytest.mark.gpu
+@every_division
+def test_one_softmax_for_all_value_columns(n, H, topk):
+    """Rows whose value columns 256-511 repeat columns 0-255: so does every result, bit for bit, although q differs."""
+    kv = latent(500, 17)
+    kv[:, 256:DV] = kv[:, :256]
+    cache, rows = store(kv)
+    q = (2 * torch.randn(n, H, D, generator=gen(18))).to(torch.bfloat16).cuda()
+    idx = torch.randint(-20, 500, (n, topk), generator=gen(19)).clamp(min=-1).to(torch.int32).cuda()
+    got = dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV)
+    assert torch.equal(got[:, :, :256], got[:, :, 256:])
+    ref, tol = attend64(q, rows, idx)
+    check(got, ref, tol)
+
+
+@pytest.mark.gpu
+@every_division
+def test_infinite_rope_columns(n, H, topk):
+    """A selected row with an infinite rope column: a logit of +inf makes NaN of the whole head, one of -inf is an
+    entry of no weight."""
+    kv = latent(400, 20)
+    kv[7, DV + 3] = INF                                 # in the share of one SM of a pair,
+    kv[8, DV + 40] = -INF                               # in that of the other
+    cache, rows = store(kv)
+    q = torch.randn(n, H, D, generator=gen(21)).to(torch.bfloat16)
+    q[:, :, DV + 3] = -q[:, :, DV + 3].abs() - 1        # -inf for every head ...
+    q[:, :, DV + 40] = q[:, :, DV + 40].abs() + 1
+    q[:, 0, DV + 3] = 2                                 # ... but the first and the last
+    q[:, H - 1, DV + 40] = -2
+    idx = torch.randint(9, 400, (n, topk), generator=gen(22)).to(torch.int32)
+    idx[:, 5], idx[:, topk - 2] = 7, 8
+    got = dsa.dsa_sparse_attn_int4kv(q.cuda(), cache, idx.cuda(), SCALE, DV)
+    assert torch.isnan(got[:, 0]).all() and torch.isnan(got[:, H - 1]).all()
+    used = idx.clone()
+    used[:, 5] = used[:, topk - 2] = -1
+    ref, tol = attend64(q[:, 1:H - 1], rows, used)
+    check(got[:, 1:H - 1], ref, tol)

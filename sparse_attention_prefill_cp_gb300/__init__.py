@@ -625,9 +625,17 @@ def _launch_on(stream, ref: torch.Tensor, *others):
     return (None if here and stream.cuda_stream == handle else torch.cuda.stream(stream)), stream.cuda_stream
 
 
+def _int32(**sizes: int) -> None:
+    """Refuse sizes that the C ABI's int32 arguments would take modulo 2^32."""
+    for name, v in sizes.items():
+        if not -0x80000000 <= v <= 0x7fffffff:
+            raise ValueError(f"{name} = {v} is not below 2^31")
+
+
 @functools.lru_cache(maxsize=None)
 def dsa_kv_int4_row_bytes(D: int, Dv: int) -> int:
     """Bytes of one 4-bit latent-KV cache row (include/dsa_cp.h)."""
+    _int32(D=D, Dv=Dv)
     n = C.c_size_t()
     check(load().dsa_kv_int4_row_bytes(D, Dv, C.byref(n)), "dsa_kv_int4_row_bytes")
     return n.value
@@ -658,6 +666,7 @@ def dsa_kv_int4_quantize(kv: torch.Tensor, Dv: int, out: torch.Tensor | None = N
         _need(out, torch.uint8, "out")
         if out.dim() != 2 or out.shape[1] != rb or (slots is None and out.shape[0] < n):
             raise ValueError(f"out must be [R, {rb}] with a row for every row written")
+    _int32(n=n, R=n if out is None else out.shape[0])
     ctx, st = _launch_on(stream, kv, out, slots)
     if ctx is not None:
         ctx.__enter__()
@@ -686,6 +695,7 @@ def dsa_kv_int4_dequantize(cache: torch.Tensor, D: int, Dv: int, rows: torch.Ten
         if rows.dim() != 1:
             raise ValueError("rows must be [n]")
         n = rows.shape[0]
+    _int32(R=R, n=n)
     if out is not None:
         _need(out, torch.bfloat16, "out")
         if tuple(out.shape) != (n, D):
@@ -706,6 +716,7 @@ def dsa_kv_int4_dequantize(cache: torch.Tensor, D: int, Dv: int, rows: torch.Ten
 
 def dsa_sparse_attn_int4kv_workspace_size(n: int, H: int, topk: int) -> int:
     """Workspace bytes of dsa_sparse_attn_int4kv for ``n`` queries on the current device."""
+    _int32(n=n, H=H, topk=topk)
     b = C.c_size_t()
     check(load().dsa_sparse_attn_int4kv_workspace_size(n, H, topk, C.byref(b)), "dsa_sparse_attn_int4kv_workspace_size")
     return b.value
@@ -761,6 +772,7 @@ def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: to
             raise ValueError(f"out must be [{m}, {H}, {Dv}]")
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
+    _int32(m=m, H=H, n=n, topk=topk, R=kv_cache.shape[0], num_kv_rows=0 if slots is None else slots.shape[0])
     ctx, st = _launch_on(stream, q, kv_cache, topk_idx, attn_sink, slots, q_rows, out, workspace)
     if ctx is not None:
         ctx.__enter__()

@@ -134,3 +134,33 @@ def test_wrappers_refuse_what_is_not_on_a_gpu():
         dsa.dsa_kv_int4_dequantize(cache, 576, 512)
     with pytest.raises(ValueError):
         dsa.dsa_sparse_attn_int4kv(q, cache, idx, 0.07, 512)
+
+
+def test_sizes_past_int32_are_refused():
+    """The C ABI counts rows in int32: 2^32 + 4 of them are not 4.  (Tensors without memory.)"""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    big = 2 ** 32 + 4
+    for call in (lambda: dsa.dsa_kv_int4_row_bytes(2 ** 32 + 576, 512),
+                 lambda: dsa.dsa_kv_int4_row_bytes(576, 512 - 2 ** 32),
+                 lambda: dsa.dsa_sparse_attn_int4kv_workspace_size(big, 128, 2048)):
+        with pytest.raises(ValueError, match="below 2\\^31"):
+            call()
+
+    def t(dtype, *shape):
+        return torch.empty(shape, dtype=dtype, device="cuda")
+
+    bf, u8, i32 = torch.bfloat16, torch.uint8, torch.int32
+    with FakeTensorMode():
+        q, cache, idx = t(bf, 4, 16, 576), t(u8, 64, 432), t(i32, 4, 64)
+        out = t(bf, 4, 16, 512)
+        for call in (lambda: dsa.dsa_kv_int4_quantize(t(bf, big, 8), 8),
+                     lambda: dsa.dsa_kv_int4_quantize(t(bf, 4, 8), 8, t(u8, big, 32)),
+                     lambda: dsa.dsa_kv_int4_dequantize(t(u8, big, 32), 8, 8),
+                     lambda: dsa.dsa_kv_int4_dequantize(t(u8, 64, 32), 8, 8, rows=t(i32, big)),
+                     lambda: dsa.dsa_sparse_attn_int4kv(q, t(u8, big, 432), idx, 0.07, 512),
+                     lambda: dsa.dsa_sparse_attn_int4kv(q, cache, idx, 0.07, 512, slots=t(i32, big)),
+                     lambda: dsa.dsa_sparse_attn_int4kv(q, cache, t(i32, big, 64), 0.07, 512, q_rows=t(i32, big),
+                                                        out=out),
+                     lambda: dsa.dsa_sparse_attn_int4kv(q, cache, t(i32, 4, big), 0.07, 512)):
+            with pytest.raises(ValueError, match="below 2\\^31"):
+                call()

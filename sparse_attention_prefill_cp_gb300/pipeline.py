@@ -226,15 +226,16 @@ class DSAPrefill:
             e1.record(st)
             ev.append((r, e0, e1))
 
-    def latent_kv(self, kv, stream=None):
+    def latent_kv(self, kv, stream=None, kv_slots=None):
         """The bf16 latent rows the attention reads: ``kv`` itself, or the
-        rows a cache stands for (dequantised into a buffer of this object)."""
+        rows a cache stands for (dequantised into a buffer of this object;
+        ``kv_slots``: the 4-bit cache's row of every KV row, as for ``run``)."""
         if self.kv_rows is None:
             return kv
         if self.kv_int4:
-            if self._kv_slots is None and kv.shape[0] != self.num_kv_rows:
+            if kv_slots is None and kv.shape[0] != self.num_kv_rows:
                 raise ValueError("without kv_slots the cache must hold the batch's KV rows in order")
-            return dsa_kv_int4_dequantize(kv, self.D, self.Dv, self._kv_slots, self.kv_rows, stream)
+            return dsa_kv_int4_dequantize(kv, self.D, self.Dv, kv_slots, self.kv_rows, stream)
         return dsa_kv_fp8_dequantize(kv, self.D, self.Dv, self.kv_rows, stream)
 
     def side_streams(self):
@@ -279,7 +280,9 @@ class DSAPrefill:
         "core_end", "end") recorded around the indexer/top-k/attention core.
         ``kv_ori``: the original latent rows for the sliding window at
         compress_ratio > 1 (at ratio 1 the window reads ``kv``).
-        ``kv_slots``: the cache row of every KV row (kv_int4)."""
+        ``kv_slots``: the cache row of every KV row (kv_int4), none negative:
+        a KV row without one would be a row of zeros to the attention over
+        dequantised rows, and unused with ``kv_int4_direct``."""
         self._take_slots(kv_slots)
         if self.window and self.compress_ratio > 1 and kv_ori is None:
             raise ValueError("the sliding window over compressed KV needs the original rows (kv_ori)")
@@ -293,7 +296,7 @@ class DSAPrefill:
         if "core_start" in ev:
             ev["core_start"].record(s)
         self._q = q
-        kv = self.latent_kv(kv, s)
+        kv = self.latent_kv(kv, s, kv_slots)
         self.views(kv, k_idx, sink, s)
         if "core_end" in ev:
             ev["core_end"].record(s)
@@ -326,7 +329,7 @@ class DSAPrefill:
         self.split(q, q_idx, w, stream)
         if self.fused:  # the head-sharded attention reads the split q
             dsa_cp_split(q, self.cp_size, self.mode, -1, self.q_split, stream)
-        kv = self.latent_kv(kv, stream)
+        kv = self.latent_kv(kv, stream, kv_slots)
         for r in range(self.cp_size):
             self.indexer(r, k_idx, stream)
             dsa_sparse_attn_prefill_headsharded(self.md[r], self.q_split[r], kv, self.topk_idx[r], self.scale,

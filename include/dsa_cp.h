@@ -596,6 +596,14 @@ dsa_status dsa_kv_int4_dequantize(const void *cache, int32_t num_cache_rows, int
  * may run at the same time need a workspace each. */
 dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H, int32_t topk, size_t *bytes);
 
+/* Host only (the current device's SM count enters).  How that call is divided:
+ * into how many splits of the entries, into groups of how many heads (0: two
+ * SMs on all heads of a query), and whether the queries with the longest lists
+ * are taken first (1, else 0).  The result does not depend on it but for
+ * roundings.  Any of the pointers may be NULL. */
+dsa_status dsa_sparse_attn_int4kv_division(int32_t n, int32_t H, int32_t topk, int32_t *splits, int32_t *group_heads,
+                                           int32_t *longest_first);
+
 /*
  * MLA sparse attention over the 4-bit cache, for any number of queries down to
  * a single token, without CP metadata: for query i and head h, over the entries

@@ -28,7 +28,8 @@ __all__ = [
     "dsa_sparse_attn_prefill", "dsa_sparse_attn_prefill_headsharded", "dsa_sparse_attn_prefill_rows",
     "dsa_swa_index",
     "dsa_sparse_attn_prefill_swa", "dsa_kv_int4_row_bytes", "dsa_kv_int4_quantize", "dsa_kv_int4_dequantize",
-    "dsa_sparse_attn_int4kv_workspace_size", "dsa_sparse_attn_int4kv", "dsa_poll_device_error",
+    "dsa_sparse_attn_int4kv_workspace_size", "dsa_sparse_attn_int4kv_division", "dsa_sparse_attn_int4kv",
+    "dsa_poll_device_error",
 ]
 
 
@@ -720,6 +721,16 @@ def dsa_sparse_attn_int4kv_workspace_size(n: int, H: int, topk: int) -> int:
     b = C.c_size_t()
     check(load().dsa_sparse_attn_int4kv_workspace_size(n, H, topk, C.byref(b)), "dsa_sparse_attn_int4kv_workspace_size")
     return b.value
+
+
+def dsa_sparse_attn_int4kv_division(n: int, H: int, topk: int) -> tuple[int, int, bool]:
+    """(splits, group_heads, longest_first) of dsa_sparse_attn_int4kv for
+    ``n`` queries on the current device; group_heads 0: two SMs on all heads."""
+    _int32(n=n, H=H, topk=topk)
+    s, g, o = C.c_int32(), C.c_int32(), C.c_int32()
+    check(load().dsa_sparse_attn_int4kv_division(n, H, topk, C.byref(s), C.byref(g), C.byref(o)),
+          "dsa_sparse_attn_int4kv_division")
+    return s.value, g.value, bool(o.value)
 
 
 @functools.lru_cache(maxsize=4096)

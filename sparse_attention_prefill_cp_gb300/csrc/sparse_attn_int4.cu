@@ -885,6 +885,17 @@ extern "C" dsa_status dsa_sparse_attn_int4kv_workspace_size(int32_t n, int32_t H
   return DSA_OK;
 }
 
+extern "C" dsa_status dsa_sparse_attn_int4kv_division(int32_t n, int32_t H, int32_t topk, int32_t *splits,
+                                                      int32_t *group_heads, int32_t *longest_first) {
+  if (n < 0 || topk < 1 || topk > kMaxTopk) return DSA_ERR_SHAPE;
+  if (H < 1 || H > kHeads) return DSA_ERR_UNSUPPORTED;
+  const Division d = divide(n, H, topk);
+  if (splits) *splits = d.splits;
+  if (group_heads) *group_heads = d.group_heads;
+  if (longest_first) *longest_first = d.ordered ? 1 : 0;
+  return DSA_OK;
+}
+
 extern "C" dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, const int32_t *q_rows, int32_t n,
                                              const void *kv_cache, int32_t num_cache_rows, const int32_t *slots,
                                              int32_t num_kv_rows, const int32_t *topk_idx, int32_t topk,

@@ -164,3 +164,18 @@ def test_sizes_past_int32_are_refused():
                      lambda: dsa.dsa_sparse_attn_int4kv(q, cache, t(i32, 4, big), 0.07, 512)):
             with pytest.raises(ValueError, match="below 2\\^31"):
                 call()
+
+
+def test_division_of_a_call(lib):
+    """Splits cover the entries, groups only up to 32 heads, and the workspace follows from the division."""
+    for n, H, topk in [(0, 128, 64), (1, 1, 1), (1, 128, 2048), (8, 128, 2048), (64, 16, 2048), (300, 128, 130),
+                       (200, 64, 1100), (2048, 128, 2048), (3, 37, 5003)]:
+        splits, heads, first = dsa.dsa_sparse_attn_int4kv_division(n, H, topk)
+        assert 1 <= splits <= 32 and splits <= -(-topk // (128 if heads else 64)) and heads in (0, 16, 32)
+        assert not first or (splits == 1 and heads == 0)
+        want = 4 * n if first else n * splits * H * (512 * 4 + 16) if splits > 1 else 0
+        assert dsa.dsa_sparse_attn_int4kv_workspace_size(n, H, topk) == want
+    f = lib.dsa_sparse_attn_int4kv_division
+    assert f(4, 128, 64, None, None, None) == 0
+    assert f(-1, 128, 64, None, None, None) == 2 and f(4, 128, 0, None, None, None) == 2
+    assert f(4, 0, 64, None, None, None) == 3 and f(4, 129, 64, None, None, None) == 3

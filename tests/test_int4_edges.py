@@ -15,6 +15,7 @@ sum_d |q_d k_d| at the very worst.  Where q and k are integers whose sums stay
 below 2^24, q.k is exact and d_j is what the scale and the exponent's fma
 round, 2^-21 of the largest logit.
 """
+import numpy as np
 import pytest
 import torch
 
@@ -95,6 +96,19 @@ def check(got, ref, tol):
     # the roundings are independent: their norm stays well below the sum of their bounds
     norm = ref.norm()
     assert norm == 0 or (got.double() - ref).norm() / norm <= 1e-2
+
+
+def division(n, H, topk):
+    splits, heads, first = dsa.dsa_sparse_attn_int4kv_division(n, H, topk)
+    return ("pairs" if heads == 0 else f"groups of {heads}") + (", split" if splits > 1 else "") + \
+        (", longest first" if first else "")
+
+
+@pytest.mark.gpu
+def test_divisions_are_what_their_names_say():
+    """What is tested below in every division is: the rule that divides a call may move, the tests then move along."""
+    for name, (n, H, topk) in DIVISIONS.items():
+        assert division(n, H, topk) == name
 
 
 # ------------------------------------------------------------------ queries without a row
@@ -221,3 +235,123 @@ def test_infinite_rope_columns(n, H, topk):
     used[:, 5] = used[:, topk - 2] = -1
     ref, tol = attend64(q[:, 1:H - 1], rows, used)
     check(got[:, 1:H - 1], ref, tol)
+
+
+# ------------------------------------------------------------------ what splits and their join have to hold
+
+# n, H, topk: decode batches whose entries are split, but for the first between pairs; odd head counts and lengths
+SPLIT = [(5, 128, 2048), (8, 128, 2048), (16, 128, 2048), (38, 128, 2048), (32, 64, 2048), (12, 100, 1500),
+             (11, 127, 1999), (7, 128, 9001)]
+
+
+def lists(n, topk, R, seed, kind):
+    g = gen(seed)
+    idx = torch.randint(0, R, (n, topk), generator=g).to(torch.int32)
+    if kind == "ragged":            # most splits of most queries have no entry, some queries none at all
+        lens = torch.exp(torch.rand(n, generator=g) * np.log(topk)).long()
+        lens[0], lens[n // 2] = topk, 0
+        idx[torch.arange(topk)[None] >= lens[:, None]] = -1
+    elif kind == "holes":
+        idx[torch.rand(n, topk, generator=g) < 0.5] = -1
+    elif kind == "tail only":       # the entries of the last split alone, one of them in the first query
+        idx[:, :topk - 3] = -1
+        idx[0, :topk - 1] = -1
+    return idx
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["full", "ragged", "holes", "tail only"])
+@pytest.mark.parametrize("n,H,topk", SPLIT)
+def test_split_entries(n, H, topk, kind):
+    """Slots (some without a row), q rows in another order, a sink; eager, again, and replayed over other lists."""
+    assert division(n, H, topk) == ("groups of 32, split" if n == 5 else "pairs, split")
+    R, KV, m = 4000, 3000, n + 3
+    cache, rows = store(latent(R, 30))
+    g = gen(31 + n)
+    slots = torch.randperm(R, generator=g)[:KV].to(torch.int32)
+    slots[::53] = -1
+    slots = slots.cuda()
+    q_rows = torch.randperm(m, generator=g)[:n].to(torch.int32)
+    q_rows[n - 1] = -1
+    at = q_rows[:n - 1].long().cuda()
+    q_rows = q_rows.cuda()
+    q = torch.randn(m, H, D, generator=g).to(torch.bfloat16).cuda()
+    sink = torch.randn(H, generator=g).cuda()
+    idx = lists(n, topk, KV, 32, kind).cuda()
+    out = torch.full((m, H, DV), 5.0, dtype=torch.bfloat16, device="cuda")
+
+    def run():
+        return dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV, attn_sink=sink, slots=slots, q_rows=q_rows, out=out)
+
+    def verify():
+        ref, tol = attend64(q[at], rows, idx[:n - 1], sink, slots)
+        check(out[at], ref, tol)
+        rest = torch.ones(m, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert (out[rest] == 5.0).all()
+
+    run()
+    verify()
+    first = out.clone()
+    run()
+    assert torch.equal(out, first)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    out.fill_(5.0)
+    idx.copy_(lists(n, topk, KV, 33, "ragged" if kind == "full" else "full"))
+    graph.replay()
+    verify()
+
+
+@pytest.mark.gpu
+@every_division
+def test_bad_entries_of_every_division(n, H, topk):
+    """An entry past the cache, past the slots, a slot past the cache and a q row past q: reported, and unused."""
+    cache, rows = store(latent(100, 34))
+    q = torch.randn(n, H, D, generator=gen(35)).to(torch.bfloat16)
+    idx = torch.randint(0, 100, (n, topk), generator=gen(36)).to(torch.int32)
+    fine = idx.clone()
+    at = (n - 1, topk - 1)
+    idx[at], fine[at] = 100, -1
+    ref, tol = attend64(q, rows, fine)
+    q, idx, fine = q.cuda(), idx.cuda(), fine.cuda()
+
+    def reported(site, got, ref, tol):
+        with pytest.raises(dsa.DSAError) as err:
+            dsa.dsa_poll_device_error()
+        assert err.value.status == 7 and err.value.detail[0] == site
+        check(got, ref, tol)
+
+    reported(50, dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV), ref, tol)
+    slots = torch.arange(100, dtype=torch.int32).cuda()
+    reported(49, dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV, slots=slots), ref, tol)
+    slots = torch.arange(101, dtype=torch.int32).cuda()
+    reported(50, dsa.dsa_sparse_attn_int4kv(q, cache, idx, SCALE, DV, slots=slots), ref, tol)
+    out = torch.zeros(n, H, DV, dtype=torch.bfloat16, device="cuda")
+    q_rows = torch.arange(n, dtype=torch.int32)
+    q_rows[0] = n
+    ref[0] = 0
+    reported(51, dsa.dsa_sparse_attn_int4kv(q, cache, fine, SCALE, DV, q_rows=q_rows.cuda(), out=out), ref, tol)
+
+
+@pytest.mark.gpu
+@every_division
+def test_large_logits_of_every_division(n, H, topk):
+    """Logits of hundreds, whose sums are exact (multiples of 2^-6 below 2^18): the running maximum moves in every block (later rows
+    larger), or the first entry outweighs the rest; a sink far above every logit, at their level, and far below."""
+    R = min(topk, 700)
+    size = torch.linspace(1, 7, R).round()
+    kv = torch.randint(0, 2, (R, D), generator=gen(37)).float() * 2 - 1
+    kv[:, :DV] *= size[:, None]
+    cache, rows = store(kv.to(torch.bfloat16))
+    assert torch.equal(rows * 64, (rows * 64).round()) and rows.abs().sum(1).max() * 16 < 2 ** 18
+    q = (torch.randint(0, 2, (n, H, D), generator=gen(38)) * 32 - 16).to(torch.bfloat16)
+    up = (torch.arange(topk) * R // topk).to(torch.int32).repeat(n, 1).cuda()
+    for idx in (up, up.flip(1).contiguous()):
+        for level in (None, -1e4, 300.0, 1e4):
+            sink = None if level is None else torch.full((H,), level).cuda()
+            got = dsa.dsa_sparse_attn_int4kv(q.cuda(), cache, idx, SCALE, DV, attn_sink=sink)
+            ref, tol = attend64(q, rows, idx, sink, exact_sums=True)
+            check(got, ref, tol)

@@ -46,8 +46,8 @@
 // (about 1,900 cycles), QK, partial S to the peer, softmax, P to the peer, PV,
 // about 12,000 cycles over four stages: a block of 64 entries every 3,000
 // cycles, 1,100 of them MMA work.  76 queries of 128 heads x 2048 entries:
-// 64 us, 680 TFLOP/s; 64 queries 63 us; 2048 queries 1.52 ms, 770 TFLOP/s (0.40
-// of the measured bf16 rate).
+// 64 us, 677 TFLOP/s (rows that all share, from L2: 56 us); 64 queries 63 us;
+// 2048 queries 1.50 ms, 780 TFLOP/s (0.41 of the measured bf16 rate).
 #include "sparse_attn_int4.cuh"
 #include "internal.h"
 
@@ -380,15 +380,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     if (lane == 0) {
-      // ---------------- sends the partial S of the peer's heads
+      // ---------------- sends the partial S of the peer's heads; the wait that ends
+      // last comes last (either way round a wait that is over costs some 170 cycles)
       const uint32_t peer_recv = map_to_cta(smem_u32(smem + kOffRecv), peer);
       const uint32_t peer_full = map_to_cta(smem_u32(recv_full), peer);
       bool ok = true;
       for (int t = 0; ok && t < nb; ++t) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
+          if (w == 0 && t >= 1) ok = wait_for<true>(recv_empty, (t - 1) & 1, failed, 64, t);
           ok = ok && wait_for(&staged[w], t & 1, failed, 63, t);
-          if (w == 0 && t >= 1) ok = ok && wait_for<true>(recv_empty, (t - 1) & 1, failed, 64, t);
           if (!ok) break;
           bulk_copy_to_peer(peer_recv + w * kXHalf, smem + kOffStg + w * kXHalf, kXHalf, peer_full + 8 * w);
           bulk_commit();
@@ -408,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t peer_msg = map_to_cta(smem_u32(msg), peer), peer_full = map_to_cta(smem_u32(p_msg), peer);
       for (int t = 0; t < nb; ++t) {
         const int b = t & 1;
-        if (!wait_for(&p_own[b], (t >> 1) & 1, failed, 65, t)) break;
         if (t >= 2 && !wait_for<true>(&p_empty[b], ((t >> 1) & 1) ^ 1, failed, 77, t)) break;
+        if (!wait_for(&p_own[b], (t >> 1) & 1, failed, 65, t)) break;
         bulk_copy_to_peer(peer_msg + b * kPBytes, msg + b * kPBytes, kPMsg, peer_full + 8 * b);
         bulk_commit();
         bulk_wait_read0();

@@ -26,12 +26,11 @@ NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 
 # Per-source ptxas settings, measured: the attention kernel's pipelined loop
 # runs ~1 % faster with ptxas -O1 than with the default -O3 (same registers);
-# with -O3 the attention over the 4-bit cache takes 4 % longer on a chunk of
-# 2,048 queries (1 to 2 % less on 64 to 256), its few-heads kernel spills (32
-# heads: 89 against 78 us for 152 queries), and the join of its parts moves
-# each load to its use instead of keeping them in flight.
-SOURCE_FLAGS = {"sparse_attn.cu": ["-Xptxas", "-O1"], "sparse_attn_int4.cu": ["-Xptxas", "-O1"],
-                "sparse_attn_int4_few.cu": ["-Xptxas", "-O1"], "sparse_attn_int4_join.cu": ["-Xptxas", "-O1"]}
+# with -O3 the few-heads attention over the 4-bit cache spills (32 heads: 89
+# against 78 us for 152 queries), and the join of its parts moves each load to
+# its use instead of keeping them in flight.
+SOURCE_FLAGS = {"sparse_attn.cu": ["-Xptxas", "-O1"], "sparse_attn_int4_few.cu": ["-Xptxas", "-O1"],
+                "sparse_attn_int4_join.cu": ["-Xptxas", "-O1"]}
 
 
 def nvcc() -> str:

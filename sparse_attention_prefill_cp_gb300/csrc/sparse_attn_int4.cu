@@ -16,8 +16,8 @@
 // of 64 entries), and returns their P and the factor by which the head's O is
 // to be rescaled (8.25 KB), so that both halves of a result come from one
 // softmax over sums held in 32 bits.  (Exchanging whole partial S tiles in fp32
-// and doing every softmax twice took 36 % longer on 2,048 queries: 32 KB each
-// way at the link's 13.6 B/clk are 2,400 cycles of a block's time.)  P is bf16
+// and doing every softmax twice: 2,060 against 1,540 us for 2,048 queries; 32 KB
+// each way at the link's 13.6 B/clk are 2,400 cycles of a block's time.)  P is bf16
 // for the MMA, each entry within 2^-8 of itself; statistics, sums and O are
 // fp32.
 //
@@ -43,11 +43,11 @@
 // result does not depend on timing).
 //
 // What bounds it: the way of a block from a freed stage to the next, decoding
-// (about 1,900 cycles), QK, partial S to the peer, softmax, P to the peer, PV,
-// about 12,000 cycles over four stages: a block of 64 entries every 3,000
+// (1,500 to 2,100 cycles), QK, partial S to the peer, softmax, P to the peer,
+// PV, about 12,000 cycles over four stages: a block of 64 entries every 3,000
 // cycles, 1,100 of them MMA work.  76 queries of 128 heads x 2048 entries:
-// 64 us, 677 TFLOP/s (rows that all share, from L2: 56 us); 64 queries 63 us;
-// 2048 queries 1.50 ms, 780 TFLOP/s (0.41 of the measured bf16 rate).
+// 63 us, 690 TFLOP/s (58.7 us where all share their rows); 64 queries 62 us;
+// 2048 queries 1.54 ms, 758 TFLOP/s (0.40 of the measured bf16 rate).
 #include "sparse_attn_int4.cuh"
 #include "internal.h"
 
@@ -429,10 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // knows row 16w + l % 16; to decode, eight lanes take one row, 32 columns
     // each (one 16-byte load, two scales): lanes of one 8-lane store phase are
     // two neighbours of four rows, and fall on eight different bank groups.
-    // A row's registers are loaded for the next block as soon as this block's
-    // row is decoded, so that a freed stage is full again after the decoding
-    // alone; slots are fetched one block before that, entries two.  An entry
-    // that names no row reads nothing; its factors are zero.
+    // The next block's codes and scales are requested before this block's are
+    // decoded (row by row as they are: up to 1.5 % slower), so that a freed stage is
+    // full again after the decoding alone; slots are fetched one block before
+    // that, entries two.  An entry that names no row reads nothing; its factors
+    // are zero.
     const int w = warp - kFirstGatherWarp;
     // the lane's place in a stage for row 4q + r4 and unit u of its four, less 512 q: place[(q & 1) * 4 + u]
     uint32_t place[8];
@@ -455,6 +456,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                       ((j != 1 && j != 2) || wait_for(q_ready, 0, failed, 67, j));
       if (!__all_sync(0xffffffffu, go)) break;
       if (lane == 0) masks[4 * s + w] = static_cast<uint16_t>(used);
+      uint4 now[4];
+      uint32_t now_scales[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        now[q] = code[q];
+        now_scales[q] = scales[q];
+        load(q, row_next);
+      }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {  // the rope columns: bf16 in the cache, four 16-byte units a row for this CTA
         const int rl = 8 * x + (lane >> 2), r = 16 * w + rl, u = lane & 3;
@@ -468,10 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = 0; q < 4; ++q) {
         const uint32_t fac = __shfl_sync(0xffffffffu, factors, 4 * q + r4);
         const uint32_t f1 = __byte_perm(fac, 0, 0x1010), f2 = __byte_perm(fac, 0, 0x3232);
-        const uint32_t words[4] = {code[q].x, code[q].y, code[q].z, code[q].w};
+        const uint32_t words[4] = {now[q].x, now[q].y, now[q].z, now[q].w};
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          const uint32_t sc = int4_scale(__byte_perm(scales[q], 0, b == 0 ? 0x4040 : 0x4141), f1, f2);
+          const uint32_t sc = int4_scale(__byte_perm(now_scales[q], 0, b == 0 ? 0x4040 : 0x4141), f1, f2);
           const uint32_t sc24 = int4_scale24(sc);
 #pragma unroll
           for (int u = 2 * b; u < 2 * b + 2; ++u) {
@@ -480,7 +489,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_v4(sb + place[(q & 1) * 4 + u] + 512 * q, o[0], o[1], o[2], o[3]);
           }
         }
-        load(q, row_next);
       }
       cp_async_wait<0>();
       fence_proxy_async_smem();
@@ -785,8 +793,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 //   a wave of 32-head CTAs 4.5 + 4.1 per block of 128
 //   joining splits         3 + the parts written and read at 5 TB/s
 // Measured with each way forced (pairs / groups of 16 / of 32, us, rows in L2):
-//   128 heads,  1 query   15.6 /  11.5 /  12.6    128 heads, 64 queries  60.7 / 228 / 120
-//    32 heads, 64 queries 56.8 /  54.1 /  38.4     16 heads, 64 queries  55.9 /  33 /  35
+//   128 heads,  1 query   15.4 /  11.5 /  13.0    128 heads, 64 queries  59.6 / 230 / 120
+//    32 heads, 64 queries 56.5 /  54.4 /  38.3     16 heads, 64 queries  56.2 /  33 /  35
 // Pairs win where there are many heads and enough queries for the SMs, groups up
 // to 32 heads, and for a query or two of many heads, whose splits alone do not
 // fill the SMs.
@@ -795,10 +803,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // their lists' lengths (sparse_attn_int4_order.cu; one more load before a pair
 // can start, and a small launch).  us for 2048 entries and 128 heads, lengths
 // log-uniform to 3000 / all lists full, in the order given -> longest first:
-//   152 queries  82.0 -> 65.4 / 126 -> 130     256  114 -> 86 / 248 -> 253
-// One wave and a half gains little more than it costs (100 queries 70.7 -> 63.9
-// / 120 -> 124), lists of 512 the less (200 queries 52.8 -> 50.6 / 72 -> 77); of
-// many waves the last matters little (1000 queries: 318 -> 315 / 858 -> 885),
+//   152 queries  79.7 -> 64.2 / 124 -> 128     256  111 -> 83 / 245 -> 251
+// One wave and a half gains little more than it costs (100 queries 69.3 -> 62.9
+// / 117 -> 122), lists of 512 the less (200 queries 51.7 -> 49.2 / 70 -> 75); of
+// many waves the last matters little (1000 queries: 311 -> 310 / 853 -> 880),
 // and groups of 16 heads pay more for the load (400 queries 86 -> 68 / 180 ->
 // 191).
 struct Division {

@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // there and O is rescaled for it; each stream in order.  The whole warp runs
     // the loop and one elected lane issues: descriptors and addresses then live
     // in uniform registers (alone on the SM, with a commit after every eight, an
-    // MMA of N = 64 takes 48 cycles so; 59 from a branch of one lane).
+    // MMA of N = 64 takes 48 to 50 cycles so; 55 to 59 from a branch of one lane).
     const bool issuer = elect_one();
     const uint32_t st_addr = smem_u32(smem + kOffStage);
     const uint64_t qk_b0 = smem_desc(st_addr, 16, 1024, kLayoutSW128);

@@ -276,8 +276,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // as they are decoded, then PV, which hands the tiles back one by one.  The
     // whole warp runs the loops and one elected lane issues: descriptors and
     // addresses then live in uniform registers (alone on the SM, with a commit
-    // after every eight, an MMA of N = 16 takes 42 cycles so; 59 from a branch of
-    // one lane).
+    // after every eight, an MMA of N = 16 takes 42 to 45 cycles so; 55 to 59 from
+    // a branch of one lane).
     const bool issuer = elect_one();
     const uint32_t tile_addr = smem_u32(smem + C::kOffTiles);
     const uint64_t k_a = smem_desc(tile_addr, 16, 1024, kLayoutSW128);

@@ -641,6 +641,119 @@ dsa_status dsa_sparse_attn_int4kv(const void *q, int32_t num_q_rows, const int32
                                   const float *attn_sink, float softmax_scale, int32_t H, int32_t D, int32_t Dv,
                                   void *out, void *workspace, size_t ws_bytes, dsa_stream_t stream);
 
+/*
+ * The paged latent cache: bf16 rows in pages of P = page_size rows (16, 32, 64
+ * or 128; else DSA_ERR_UNSUPPORTED), and beside it the index keys of the same
+ * rows and one mean index key per page.  page_table int32 [batch][max_pages]
+ * (batch * max_pages < 2^31): position p of request b lies in slot
+ *   page_table[b][p / P] * P + p % P,
+ * row p % P of that page.  Entries behind a request's last page are -1.
+ */
+
+/*
+ * Page tables for new lengths: request b had pages for its first held_lens[b]
+ * rows and gets pages for seq_lens[b] (shorter: the pages behind are released,
+ * their entries become -1).  free_pages int32 [num_pages] is a stack of free
+ * page numbers, free_count int32 [1] (device) how many it holds.  With R pages
+ * released and G taken, both numbered request by request and page by page, and
+ * c = *free_count before: released page j is written to free_pages[c + R - 1 -
+ * j], then taken page k is read from free_pages[c + R - 1 - k], and *free_count
+ * becomes c + R - G.  A call with held_lens and seq_lens exchanged undoes one.
+ * All or nothing: a length below 0 or beyond max_pages * P (detail: the
+ * request), a released entry that is no page of 0 .. num_pages - 1 (the
+ * request), or too few free pages (G) is a DSA_ERR_DEVICE_BOUNDS and changes
+ * nothing.
+ */
+dsa_status dsa_pages_update(int32_t *page_table, int32_t batch, int32_t max_pages, const int32_t *held_lens,
+                            const int32_t *seq_lens, int32_t page_size, int32_t *free_pages, int32_t num_pages,
+                            int32_t *free_count, dsa_stream_t stream);
+
+/* Slots of the positions first_pos[b] .. seq_lens[b] - 1 (first_pos NULL: from
+ * 0) of every request, requests in order, into slots[num_slots]; -1 behind the
+ * last and for positions whose page the table does not have.  These are the
+ * `slots` of the calls below and, with first_pos NULL, of the 4-bit cache's
+ * attention (KV rows in request order).  More positions than num_slots, a
+ * negative first_pos or seq_lens (taken as 0), or a length beyond max_pages * P
+ * is a DSA_ERR_DEVICE_BOUNDS. */
+dsa_status dsa_pages_slots(const int32_t *page_table, int32_t batch, int32_t max_pages, const int32_t *first_pos,
+                           const int32_t *seq_lens, int32_t page_size, int32_t *slots, int32_t num_slots,
+                           dsa_stream_t stream);
+
+/*
+ * Write rows into their slots.  Row i of kv (bf16, D columns, rows kv_stride
+ * elements apart) becomes row slots[i] of cache: page slots[i] / P starts
+ * page_stride elements after the page before, its rows lie row_stride apart
+ * (all strides multiples of 8, at least D).  With k_idx (bf16 [n][DI], DI a
+ * multiple of 8 up to 128; NULL: latent rows only), key_cache bf16
+ * [num_pages][P][DI] gets the index keys likewise, and where a page's last row
+ * (slot % P == P - 1) is written, block_keys bf16 [num_pages][DI] gets the mean
+ * of the page's P keys: fp32 sum, in an order that does not depend on which call
+ * wrote which row, rounded once to bf16.  A negative slot leaves its row
+ * unwritten; a slot beyond the pages is a DSA_ERR_DEVICE_BOUNDS and not
+ * written.  The slots of a call are distinct, and those of one page stand
+ * together, ascending and without gaps (as dsa_pages_slots makes them).
+ */
+dsa_status dsa_pages_append(const void *kv, int64_t kv_stride, const void *k_idx, const int32_t *slots, int32_t n,
+                            int32_t D, int32_t DI, void *cache, int64_t page_stride, int64_t row_stride,
+                            int32_t num_pages, int32_t page_size, void *key_cache, void *block_keys,
+                            dsa_stream_t stream);
+
+/*
+ * For every query the pages worth reading: query i (request req[i], or i where
+ * req is NULL: then n <= batch) sees the first lens[i] positions, that is
+ * ceil(lens[i] / P) pages.  The first keep_first and the last keep_last (>= 1)
+ * of them are taken, then those with the highest
+ *   S[i, b] = sum_j w[i, j] relu(q_idx[i, j, :] . block_keys[page_table[.][b], :])
+ * ties to the lower b, up to nsel pages (keep_first + keep_last <= nsel).
+ *   q_idx  bf16 [n][HI][DI], DI = 128, HI <= 64;  w fp32 [n][HI]
+ *   blocks int32 [n][nsel]: their ordinals b, ascending, -1 behind the last
+ * With at most nsel pages all are taken.  A NaN score ranks below every number.
+ * A negative lens[i] is no query: its row of blocks keeps its values.  A request
+ * or length that the table does not have, and a page number that is none, are
+ * DSA_ERR_DEVICE_BOUNDS (such a page ranks last).  A query's scores are kept in
+ * shared memory: max_pages up to 37,000 (DSA_ERR_UNSUPPORTED beyond).
+ */
+dsa_status dsa_block_select(const void *q_idx, const float *w, int32_t n, int32_t HI, int32_t DI,
+                            const void *block_keys, int32_t num_pages, int32_t page_size, const int32_t *page_table,
+                            int32_t batch, int32_t max_pages, const int32_t *lens, const int32_t *req, int32_t nsel,
+                            int32_t keep_first, int32_t keep_last, int32_t *blocks, dsa_stream_t stream);
+
+/* Host only (the current device's SM count enters).  Workspace bytes of
+ * dsa_paged_attn (nsel 0: without blocks).  Calls that may run at the same time
+ * need a workspace each. */
+dsa_status dsa_paged_attn_workspace_size(int32_t n, int32_t H, int32_t max_pages, int32_t nsel, int32_t page_size,
+                                         size_t *bytes);
+
+/*
+ * MLA attention over the paged cache, for any number of queries down to one
+ * token: query i (request req[i], or i where req is NULL: then n <= batch) sees
+ * the positions p < lens[i] of its request, or with blocks those of them in the
+ * pages blocks[i, :] (ordinals b of the request's pages; the used ones first,
+ * distinct; a negative one ends the list), and for every head h
+ *   l_p = softmax_scale * q[i, h, :] . k_p
+ *   out[i, h, :] = sum_p e^(l_p - m) k_p[:Dv] / (sum_p e^(l_p - m) + e^(sink_h - m))
+ *   q          bf16 [n][H][D];  out bf16 [n][H][Dv];  attn_sink fp32 [H] or NULL
+ *   cache      bf16 rows of D columns, row_stride elements apart in a page, pages
+ *              page_stride apart (multiples of 8)
+ *   blocks     int32 [n][nsel], or NULL with nsel 0
+ *   workspace  at least dsa_paged_attn_workspace_size bytes, 16-byte aligned (else
+ *              DSA_ERR_WORKSPACE); written and read within the call
+ * A query with lens[i] = 0 or no used page gets zeros, one with lens[i] < 0 is
+ * none and leaves its rows of out as they are.  Rows of a page behind a query's
+ * last position may hold anything.  A request or length that the table does not
+ * have and a page number that is none are DSA_ERR_DEVICE_BOUNDS, and their rows
+ * unused.  D = 576, Dv = 512, 1 <= H <= 128 (DSA_ERR_UNSUPPORTED otherwise),
+ * softmax_scale > 0 and finite.  bf16 products with fp32 sums, softmax in fp32
+ * but for the weights that multiply the values (bf16, each within 2^-8 of
+ * itself).  The work is divided by the lengths, on the device, and parts are
+ * joined in a fixed order: the same inputs give the same bits.
+ */
+dsa_status dsa_paged_attn(const void *q, int32_t n, const void *cache, int64_t page_stride, int64_t row_stride,
+                          int32_t num_pages, int32_t page_size, const int32_t *page_table, int32_t batch,
+                          int32_t max_pages, const int32_t *lens, const int32_t *req, const int32_t *blocks,
+                          int32_t nsel, const float *attn_sink, float softmax_scale, int32_t H, int32_t D, int32_t Dv,
+                          void *out, void *workspace, size_t ws_bytes, dsa_stream_t stream);
+
 /* Synchronise `stream`, then return (and clear) the first error a kernel
  * recorded on the current device since the last poll: DSA_OK, or
  * DSA_ERR_DEVICE_TIMEOUT / _BOUNDS / _SEQ_LENS; DSA_ERR_CUDA if the sync
@@ -654,7 +767,11 @@ dsa_status dsa_poll_device_error(dsa_stream_t stream);
  * slot, top-k overflow, attention slot, attention index, metadata), 47-51
  * bounds checks around the 4-bit cache (written slot, row read back, index
  * entry, its cache row, query row; the detail is the position in the list),
- * 60-79 waits of the attention over it (the detail is the key block). */
+ * 60-79 waits of the attention over it (the detail is the key block); 52-58
+ * bounds checks around the paged cache (52 a length, 53 a released page, 54 free
+ * pages, 55 slots, 56 a written slot, 57 a page number, 58 a query's request or
+ * length; the detail is the request, the row or the query), 80-92 waits of the
+ * attention over it, 93 of the block selection. */
 dsa_status dsa_poll_device_error_detail(dsa_stream_t stream, int32_t *detail);
 
 /* Static string for a status code. */

@@ -9,6 +9,7 @@ PyTorch only provides device memory and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import functools
 
@@ -29,7 +30,8 @@ __all__ = [
     "dsa_swa_index",
     "dsa_sparse_attn_prefill_swa", "dsa_kv_int4_row_bytes", "dsa_kv_int4_quantize", "dsa_kv_int4_dequantize",
     "dsa_sparse_attn_int4kv_workspace_size", "dsa_sparse_attn_int4kv_division", "dsa_sparse_attn_int4kv",
-    "dsa_poll_device_error",
+    "dsa_pages_update", "dsa_pages_slots", "dsa_pages_append", "dsa_block_select", "dsa_paged_attn_workspace_size",
+    "dsa_paged_attn", "dsa_poll_device_error",
 ]
 
 
@@ -626,6 +628,9 @@ def _launch_on(stream, ref: torch.Tensor, *others):
     return (None if here and stream.cuda_stream == handle else torch.cuda.stream(stream)), stream.cuda_stream
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _int32(**sizes: int) -> None:
     """Refuse sizes that the C ABI's int32 arguments would take modulo 2^32."""
     for name, v in sizes.items():
@@ -802,6 +807,242 @@ def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: to
     finally:
         if ctx is not None:
             ctx.__exit__(None, None, None)
+    return out
+
+
+PAGE_SIZES = (16, 32, 64, 128)
+
+
+def _page_size(P: int) -> int:
+    if P not in PAGE_SIZES:
+        raise ValueError(f"pages of {P} rows: a page has one of {PAGE_SIZES}")
+    return int(P)
+
+
+def _need_table(page_table: torch.Tensor) -> tuple[int, int]:
+    _need(page_table, torch.int32, "page_table")
+    if page_table.dim() != 2 or page_table.shape[1] < 1:
+        raise ValueError("page_table must be [batch, max_pages]")
+    _int32(table_entries=page_table.numel())
+    return tuple(page_table.shape)
+
+
+def _need_ints(t: torch.Tensor | None, n: int, name: str) -> None:
+    if t is not None:
+        _need(t, torch.int32, name)
+        if tuple(t.shape) != (n,):
+            raise ValueError(f"{name} must be [{n}]")
+
+
+def _pages(t: torch.Tensor, name: str) -> tuple[int, int, int, int, int]:
+    """(pages, rows, columns, page stride, row stride) of a bf16 [pages, P, D]
+    tensor whose rows are contiguous and start on 16-byte boundaries."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+        raise ValueError(f"{name} must be a CUDA bfloat16 tensor [num_pages, page_size, D]")
+    R, P, D = t.shape
+    _page_size(P)
+    _int32(rows=R * P)
+    row = t.stride(1)
+    page = t.stride(0) if R > 1 else row * P
+    if t.stride(2) != 1 or row < D or row % 8 or page % 8 or page < (P - 1) * row + D or t.data_ptr() % 16:
+        raise ValueError(f"the rows of {name} must be contiguous, not overlap and start on 16-byte boundaries")
+    return R, P, D, page, row
+
+
+def dsa_pages_update(page_table: torch.Tensor, held_lens: torch.Tensor, seq_lens: torch.Tensor,
+                     free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int, stream=None) -> torch.Tensor:
+    """Page tables int32 [batch, max_pages] for new lengths, in place: request
+    b has pages for its first ``held_lens``[b] rows and gets pages for
+    ``seq_lens``[b] (int32 [batch]; a shorter one gives pages back).  Pages
+    come from the stack ``free_pages`` (int32 [num_pages], ``free_count`` int32
+    [1] of them free).  Where a length is out of range or the free pages do
+    not suffice nothing changes, and dsa_poll_device_error tells; a call with
+    the lengths exchanged undoes one."""
+    B, width = _need_table(page_table)
+    P = _page_size(page_size)
+    _need_ints(held_lens, B, "held_lens")
+    _need_ints(seq_lens, B, "seq_lens")
+    _need(free_pages, torch.int32, "free_pages")
+    if free_pages.dim() != 1:
+        raise ValueError("free_pages must be [num_pages]")
+    _need_ints(free_count, 1, "free_count")
+    ctx, st = _launch_on(stream, page_table, held_lens, seq_lens, free_pages, free_count)
+    with ctx or _HERE:
+        check(load().dsa_pages_update(_addr(page_table), B, width, _addr(held_lens), _addr(seq_lens), P,
+                                      _addr(free_pages), free_pages.numel(), _addr(free_count), st), "dsa_pages_update")
+    return page_table
+
+
+def dsa_pages_slots(page_table: torch.Tensor, first: torch.Tensor | None, seq_lens: torch.Tensor, page_size: int,
+                    num_slots: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Slots int32 [num_slots] of the positions ``first``[b] .. ``seq_lens``[b]
+    - 1 of every request (``first`` None: from 0, every KV row of the batch),
+    requests in order, -1 behind the last."""
+    B, width = _need_table(page_table)
+    P = _page_size(page_size)
+    _need_ints(first, B, "first")
+    _need_ints(seq_lens, B, "seq_lens")
+    if num_slots < 0:
+        raise ValueError(f"num_slots = {num_slots}")
+    _int32(num_slots=num_slots)
+    _need_ints(out, num_slots, "out")
+    ctx, st = _launch_on(stream, page_table, first, seq_lens, out)
+    with ctx or _HERE:
+        if out is None:
+            out = torch.empty(num_slots, dtype=torch.int32, device=page_table.device)
+        check(load().dsa_pages_slots(_addr(page_table), B, width, _addr(first), _addr(seq_lens), P, _addr(out),
+                                     num_slots, st), "dsa_pages_slots")
+    return out
+
+
+def dsa_pages_append(kv: torch.Tensor, k_idx: torch.Tensor | None, slots: torch.Tensor, cache: torch.Tensor,
+                     key_cache: torch.Tensor | None = None, block_keys: torch.Tensor | None = None,
+                     stream=None) -> None:
+    """Latent rows kv bf16 [n, D] into ``slots`` (int32 [n], negative: not
+    written) of the paged ``cache`` bf16 [num_pages, P, D], and with ``k_idx``
+    bf16 [n, DI] their index keys into ``key_cache`` [num_pages, P, DI] and
+    the mean key of every page whose last row is written into ``block_keys``
+    [num_pages, DI].  Slots of one page stand together, ascending.  The rows
+    of kv and of cache may lie apart, each starting on a 16-byte boundary."""
+    R, P, D, page, row = _pages(cache, "cache")
+    if not isinstance(kv, torch.Tensor) or not kv.is_cuda or kv.dtype != torch.bfloat16 or kv.dim() != 2 or \
+            kv.shape[1] != D:
+        raise ValueError(f"kv must be a CUDA bfloat16 tensor [n, {D}]")
+    n = kv.shape[0]
+    stride = kv.stride(0) if n > 1 else D
+    if kv.stride(1) != 1 or stride < D or stride % 8 or kv.data_ptr() % 16:
+        raise ValueError("the rows of kv must be contiguous, not overlap and start on 16-byte boundaries")
+    if D < 8 or D % 8:
+        raise ValueError("D must be a multiple of 8")
+    _int32(n=n)
+    _need(slots, torch.int32, "slots")
+    _need_ints(slots, n, "slots")
+    DI = 8
+    if (k_idx is None) != (key_cache is None) or (k_idx is None) != (block_keys is None):
+        raise ValueError("k_idx, key_cache and block_keys come together")
+    if k_idx is not None:
+        for t, name in ((k_idx, "k_idx"), (key_cache, "key_cache"), (block_keys, "block_keys")):
+            _need(t, torch.bfloat16, name)
+        DI = k_idx.shape[-1]
+        if tuple(k_idx.shape) != (n, DI) or tuple(key_cache.shape) != (R, P, DI) or tuple(block_keys.shape) != (R, DI):
+            raise ValueError(f"k_idx must be [{n}, DI], key_cache [{R}, {P}, DI] and block_keys [{R}, DI]")
+    ctx, st = _launch_on(stream, cache, kv, k_idx, slots, key_cache, block_keys)
+    with ctx or _HERE:
+        check(load().dsa_pages_append(kv.data_ptr(), stride, _addr(k_idx), slots.data_ptr(), n, D, DI, cache.data_ptr(),
+                                      page, row, R, P, _addr(key_cache), _addr(block_keys), st), "dsa_pages_append")
+
+
+def dsa_block_select(q_idx: torch.Tensor, w: torch.Tensor, block_keys: torch.Tensor, page_table: torch.Tensor,
+                     lens: torch.Tensor, page_size: int, nsel: int, keep_first: int = 1, keep_last: int = 1,
+                     req: torch.Tensor | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The pages that each query reads: q_idx bf16 [n, HI, DI], w fp32 [n, HI],
+    block_keys bf16 [num_pages, DI] -> int32 [n, nsel], ordinals of its
+    request's pages, ascending, -1 behind the last.  Query i sees the first
+    ``lens``[i] positions of request ``req``[i] (None: request i); the first
+    ``keep_first`` and last ``keep_last`` of its pages are always among them,
+    the others by the indexer score of their mean keys.  A query with a
+    negative length has no row: ``out`` keeps what is there."""
+    _need(q_idx, torch.bfloat16, "q_idx")
+    _need(w, torch.float32, "w")
+    _need(block_keys, torch.bfloat16, "block_keys")
+    B, width = _need_table(page_table)
+    P = _page_size(page_size)
+    if q_idx.dim() != 3 or tuple(w.shape) != tuple(q_idx.shape[:2]):
+        raise ValueError("q_idx must be [n, HI, DI] and w [n, HI]")
+    n, HI, DI = q_idx.shape
+    if block_keys.dim() != 2 or block_keys.shape[1] != DI:
+        raise ValueError(f"block_keys must be [num_pages, {DI}]")
+    _need(lens, torch.int32, "lens")
+    _need_ints(lens, n, "lens")
+    _need_ints(req, n, "req")
+    if req is None and n > B:
+        raise ValueError("more queries than requests (pass req)")
+    _int32(n=n, rows=block_keys.shape[0] * P, blocks=n * nsel, nsel=nsel, keep_first=keep_first, keep_last=keep_last)
+    if out is not None:
+        _need(out, torch.int32, "out")
+        if tuple(out.shape) != (n, nsel):
+            raise ValueError(f"out must be [{n}, {nsel}]")
+    ctx, st = _launch_on(stream, q_idx, w, block_keys, page_table, lens, req, out)
+    with ctx or _HERE:
+        if out is None:
+            out = torch.empty((n, max(nsel, 0)), dtype=torch.int32, device=q_idx.device)
+        check(load().dsa_block_select(q_idx.data_ptr(), w.data_ptr(), n, HI, DI, block_keys.data_ptr(),
+                                      block_keys.shape[0], P, page_table.data_ptr(), B, width, lens.data_ptr(),
+                                      _addr(req), nsel, keep_first, keep_last, out.data_ptr(), st), "dsa_block_select")
+    return out
+
+
+def dsa_paged_attn_workspace_size(n: int, H: int, max_pages: int, nsel: int, page_size: int) -> int:
+    """Workspace bytes of dsa_paged_attn on the current device (nsel 0: without blocks)."""
+    _int32(n=n, H=H, max_pages=max_pages, nsel=nsel)
+    b = C.c_size_t()
+    check(load().dsa_paged_attn_workspace_size(n, H, max_pages, nsel, page_size, C.byref(b)),
+          "dsa_paged_attn_workspace_size")
+    return b.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _paged_workspace(device: int, n: int, H: int, max_pages: int, nsel: int, page_size: int) -> int:
+    return dsa_paged_attn_workspace_size(n, H, max_pages, nsel, page_size)  # with that device current
+
+
+def dsa_paged_attn(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
+                   softmax_scale: float, Dv: int, blocks: torch.Tensor | None = None, req: torch.Tensor | None = None,
+                   attn_sink: torch.Tensor | None = None, out: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """MLA attention over the paged ``cache`` bf16 [num_pages, P, D], for any
+    number of queries down to one token: q bf16 [n, H, D] -> bf16 [n, H, Dv].
+    Query i attends to the first ``lens``[i] positions of request ``req``[i]
+    (None: request i) of ``page_table`` int32 [batch, max_pages], or with
+    ``blocks`` int32 [n, nsel] to those of them in the pages that its row
+    names (ordinals of the request's pages, the used ones first, as
+    dsa_block_select makes them).  A length of 0 gives zeros, a negative one
+    leaves the query's rows of ``out`` as they are.  ``workspace``: uint8, at
+    least dsa_paged_attn_workspace_size bytes, allocated per call when
+    omitted."""
+    _need(q, torch.bfloat16, "q")
+    if q.dim() != 3:
+        raise ValueError("q must be [n, H, D]")
+    n, H, D = q.shape
+    R, P, Dc, page, row = _pages(cache, "cache")
+    if Dc != D:
+        raise ValueError("q / cache do not match in D")
+    B, width = _need_table(page_table)
+    _need(lens, torch.int32, "lens")
+    _need_ints(lens, n, "lens")
+    _need_ints(req, n, "req")
+    if req is None and n > B:
+        raise ValueError("more queries than requests (pass req)")
+    nsel = 0
+    if blocks is not None:
+        _need(blocks, torch.int32, "blocks")
+        if blocks.dim() != 2 or blocks.shape[0] != n or blocks.shape[1] < 1:
+            raise ValueError(f"blocks must be [{n}, nsel]")
+        nsel = blocks.shape[1]
+    if attn_sink is not None:
+        _need(attn_sink, torch.float32, "attn_sink")
+        if tuple(attn_sink.shape) != (H,):
+            raise ValueError(f"attn_sink must be [{H}]")
+    if out is not None:
+        _need(out, torch.bfloat16, "out")
+        if tuple(out.shape) != (n, H, Dv):
+            raise ValueError(f"out must be [{n}, {H}, {Dv}]")
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    _int32(n=n, H=H, blocks=n * nsel)
+    ctx, st = _launch_on(stream, q, cache, page_table, lens, blocks, req, attn_sink, out, workspace)
+    with ctx or _HERE:
+        if out is None:
+            out = torch.empty((n, H, Dv), dtype=torch.bfloat16, device=q.device)
+        if workspace is None:
+            ws_bytes = _paged_workspace(q.get_device(), n, H, width, nsel, P)
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+        else:
+            ws_bytes = workspace.numel()
+        check(load().dsa_paged_attn(q.data_ptr(), n, cache.data_ptr(), page, row, R, P, page_table.data_ptr(), B, width,
+                                    lens.data_ptr(), _addr(req), _addr(blocks), nsel, _addr(attn_sink),
+                                    float(softmax_scale), H, D, Dv, out.data_ptr(), workspace.data_ptr(), ws_bytes, st),
+              "dsa_paged_attn")
     return out
 
 

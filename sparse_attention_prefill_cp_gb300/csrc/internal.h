@@ -32,6 +32,9 @@ dsa_status encode_tensor_map(CUtensorMap *map, CUtensorMapDataType dtype, uint32
 
 int num_sms();
 
+// log2 of a page size of the paged latent cache (16, 32, 64 or 128 rows), -1 of any other.
+int page_shift(int32_t page_size);
+
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace dsa

@@ -1,8 +1,8 @@
 // What the two kernels of the attention over the 4-bit cache share: the call's
-// parameters, the resolution of index entries, waits without calls, and
-// single-use loads.
+// parameters, the resolution of index entries, and single-use loads.
 #pragma once
 
+#include "attn_common.cuh"
 #include "int4_common.cuh"
 
 namespace dsa {
@@ -40,38 +40,6 @@ dsa_status launch_attn_int4_order(int32_t n, const AttnInt4Params &P, int32_t *o
 
 // Launch of the kernel that joins the parts of P.splits > 1 splits.
 dsa_status launch_attn_int4_join(int32_t n, const AttnInt4Params &P, cudaStream_t stream);
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-  return r != 0;
-}
-
-// mbar_wait without a call, for the loops that hold most of the registers:
-// bounded by the same time, the failing site and detail noted in shared memory.
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, int32_t *failed, int site, int detail = 0) {
-  if (kCluster ? mbar_try_wait_hint_cluster(bar, parity) : mbar_try_wait_hint(bar, parity)) return true;
-  const long long t0 = clock64();
-  do {
-    if (kCluster ? mbar_try_wait_hint_cluster(bar, parity) : mbar_try_wait_hint(bar, parity)) return true;
-  } while (clock64() - t0 < kWaitLimitCycles);
-  *failed = site << 24 | (detail & 0xffffff);
-  return false;
-}
 
 // The cache row that an index entry names (negative: none), unchecked: the
 // value of the slot load is not looked at before checked_row.
@@ -118,15 +86,5 @@ __device__ __forceinline__ void ld_once_u8(uint32_t &r, const void *p, bool go) 
       : "+r"(r)
       : "l"(p), "r"(static_cast<uint32_t>(go)));
 }
-
-// The bulk copy of a result out of shared memory.
-__device__ __forceinline__ void bulk_store(void *dst, const void *src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-               : "memory");
-}
-
-// Until this thread's bulk copies are complete, not only read: the join of the
-// parts may be resident before this kernel has ended.
-__device__ __forceinline__ void bulk_wait_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 }  // namespace dsa

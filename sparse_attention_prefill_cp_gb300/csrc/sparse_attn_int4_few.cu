@@ -96,30 +96,6 @@ __device__ __forceinline__ bool softmax_or(bool p) {
   return r != 0;
 }
 
-// Columns of the warp's own TMEM lanes.
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
-#define DSA_OUT8(b) "=r"(r[b + 0]), "=r"(r[b + 1]), "=r"(r[b + 2]), "=r"(r[b + 3]), "=r"(r[b + 4]), "=r"(r[b + 5]), \
-                    "=r"(r[b + 6]), "=r"(r[b + 7])
-#define DSA_IN8(b) "r"(r[b + 0]), "r"(r[b + 1]), "r"(r[b + 2]), "r"(r[b + 3]), "r"(r[b + 4]), "r"(r[b + 5]), \
-                   "r"(r[b + 6]), "r"(r[b + 7])
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];"
-      : DSA_OUT8(0), DSA_OUT8(8)
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};" ::"r"(taddr),
-      DSA_IN8(0), DSA_IN8(8)
-      : "memory");
-}
-#undef DSA_OUT8
-#undef DSA_IN8
-
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     sparse_attn_int4_few_kernel(const __grid_constant__ CUtensorMap q_map, const AttnInt4Params P) {

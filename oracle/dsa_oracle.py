@@ -741,3 +741,66 @@ def prefill_swa(q, kv, q_idx, k_idx, w, query_start_loc, seq_lens, cp_size: int,
             _, _, outs[r, i] = view_row_swa(md, i, qs[r], qis[r], ws[r], kv, k_idx, topk, scale, Dv, window,
                                             kv_ori, ori_starts, sink)
     return rerange(outs, T, cp_size, mode)
+
+
+# ------------------------------------------------------------------ the paged latent cache
+
+def pages_update(table, held_lens, seq_lens, free_pages, free_count: int, page_size: int):
+    """Page tables for new lengths: (table, free_pages, free_count) after every
+    request has pages for seq_lens rows instead of held_lens.  The free list
+    is a stack: releases are pushed, the last request's last page first, so
+    that the first one lies on top; then pages are taken from the top, request
+    by request.  Returns None where it cannot be done (nothing changes)."""
+    table = [list(r) for r in table]
+    free = list(free_pages)
+    had = [-(-h // page_size) for h in held_lens]
+    need = [-(-s // page_size) for s in seq_lens]
+    width = len(table[0]) if table else 0
+    if any(x < 0 or x > width * page_size for x in list(held_lens) + list(seq_lens)):
+        return None
+    released = [(b, k) for b in range(len(table)) for k in range(need[b], had[b])]
+    taken = [(b, k) for b in range(len(table)) for k in range(had[b], need[b])]
+    top = free_count + len(released)
+    if any(not 0 <= table[b][k] < len(free) for b, k in released) or top > len(free) or len(taken) > top or \
+            free_count < 0:
+        return None
+    for n, (b, k) in enumerate(reversed(released)):
+        free[free_count + n] = table[b][k]
+        table[b][k] = -1
+    for b, k in taken:
+        top -= 1
+        table[b][k] = free[top]
+    return table, free, top
+
+
+def pages_slots(table, first, seq_lens, page_size: int, num_slots: int):
+    """Slots of positions first[b] .. seq_lens[b] - 1 of every request, -1 behind the last."""
+    out = [table[b][p // page_size] * page_size + p % page_size if table[b][p // page_size] >= 0 else -1
+           for b in range(len(seq_lens)) for p in range(first[b] if first is not None else 0, seq_lens[b])]
+    return out + [-1] * (num_slots - len(out))
+
+
+def block_select(q_idx, w, block_keys, page_row, length: int, page_size: int, nsel: int, keep_first: int = 1,
+                 keep_last: int = 1):
+    """One query's pages: the first keep_first and last keep_last of those it
+    sees, then by sum_j w_j relu(q_j . key), ties to the lower, ascending, -1
+    behind the last."""
+    have = -(-length // page_size)
+    dots = np.maximum(np.asarray(q_idx, np.float64) @ np.asarray(block_keys, np.float64)[page_row[:have]].T, 0.0)
+    score = np.asarray(w, np.float64) @ dots
+    kept = sorted({b for b in range(have) if b < keep_first or b >= have - keep_last})
+    rest = sorted((b for b in range(have) if b not in kept), key=lambda b: (-score[b], b))
+    chosen = sorted((kept + rest)[:nsel])
+    return chosen + [-1] * (nsel - len(chosen))
+
+
+def paged_attention(q, cache, page_row, length: int, scale: float, Dv: int, sink=None, blocks=None):
+    """One query [H, D] over the rows of its pages (all of them, or those named
+    in ``blocks``) at positions below ``length``; zeros where there are none."""
+    P = cache.shape[1]
+    named = None if blocks is None else {int(b) for b in blocks if b >= 0}
+    pos = [p for p in range(length) if named is None or p // P in named]
+    if not pos:
+        return np.zeros((np.asarray(q).shape[0], Dv))
+    rows = np.stack([cache[page_row[p // P], p % P] for p in pos])
+    return sparse_attention(q, rows, scale, Dv, sink)

@@ -23,6 +23,24 @@ inline dsa_status check_launch() {
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
 }
 
+// Launch of a kernel that may become resident while the kernel before it in the
+// stream still runs: it touches memory only behind griddepcontrol.wait.
+template <typename... Params, typename... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                              const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
 // rank <= 3; dims/strides in elements/bytes as the driver API expects
 // (strides exclude the innermost dimension).

@@ -25,8 +25,8 @@
 // O^T needs, handed back as soon as that step is done), one or two tiles of rope
 // columns, over which P is written once QK is done, and Q.
 //
-// Warps: softmax (one or two warpgroups, thread = row of the block = TMEM lane,
-// a warpgroup for half of the heads), MMA issue, TMA.
+// Warps: softmax (a warpgroup for every 16 heads, thread = row of the block = TMEM
+// lane), MMA issue, TMA.
 //
 // Softmax: a head's reference m lies within 2^8 of its running maximum; only
 // where a logit is above it (and in a query's first block) are the block's
@@ -46,13 +46,13 @@ constexpr int kTileBytes = 2 * kChunkBytes;  // 128 value columns
 constexpr int kTiles = kDv / 128;            // per block
 constexpr int kQChunks = kD / 64;
 
-template <int HP_, int NT_, int NR_, int WG_>
+template <int HP_, int NT_, int NR_>
 struct PagedCfg {
   static constexpr int HP = HP_;         // heads (the missing ones are zero rows of Q)
   static constexpr int NT = NT_;         // value tiles
   static constexpr int NR = NR_;         // rope tiles
-  static constexpr int WG = WG_;         // softmax warpgroups
-  static constexpr int HW = HP / WG;     // heads of a warpgroup
+  static constexpr int HW = 16;          // heads of a softmax warpgroup
+  static constexpr int WG = HP / HW;
   static constexpr int kMmaWarp = 4 * WG, kLoadWarp = kMmaWarp + 1;
   static constexpr int kWarps = kLoadWarp + 1, kThreads = 32 * kWarps;
   static constexpr int kSCol = kTiles * HP;  // TMEM: O^T, then two S buffers
@@ -72,12 +72,18 @@ struct PagedCfg {
   static constexpr uint32_t kIdescPV = idesc_bf16(128, HP, true, true);
   static_assert(kSCol + 2 * HP <= kTmemCols, "TMEM budget");
   static_assert(kOffQ % 1024 == 0 && (HP * 128) % 1024 == 0, "swizzle atoms");
-  static_assert(HW == 16 || HW == 32, "a lane holds a head's statistics");
   static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
 };
-using Cfg16 = PagedCfg<16, 5, 2, 1>;
-using Cfg32 = PagedCfg<32, 5, 1, 2>;
-using Cfg64 = PagedCfg<64, 4, 1, 2>;
+using Cfg16 = PagedCfg<16, 5, 2>;
+using Cfg32 = PagedCfg<32, 5, 1>;
+using Cfg64 = PagedCfg<64, 4, 1>;
+
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int32_t x, int32_t y, int32_t z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
 
 // OR of a predicate over the four warps of a warpgroup, and a barrier among them.
 __device__ __forceinline__ bool wg_or(int wg, bool p) {
@@ -188,6 +194,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tma_prefetch_desc(&q_map);
     tma_prefetch_desc(&kv_map);
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before may still run
   // Where the share starts: the threads sum consecutive queries' blocks, and the
   // one that holds the share's first block finds its query.
   const int per = (P.n + C::kThreads - 1) / C::kThreads;
@@ -230,6 +237,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   walk.left = g1 - g0;
   bool more = walk.start(P, misc[4], misc[5]);
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the join, which waits for this kernel's end
   if (warp == C::kLoadWarp) {
     // ---------------- TMA: lane l of a tile's boxes (chunk of 64 columns, page);
     // the pages of a block are looked up one block ahead.
@@ -297,6 +305,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         if (c_lane == 0 && there)
           tma_load_3d(smem + C::kOffRope + r * kChunkBytes + e_lane * page_bytes, &kv_map, kDv, 0, page, &r_full[r]);
         ++blk;
+        // the next block on its way to the L2 while this one is worked on
+        if ((j + 1 < j1 || again) && page_next >= 0 && page_next < P.num_pages)
+          for (int c = c_lane; c < kQChunks; c += 32 / E) tma_prefetch_3d(&kv_map, 64 * c, 0, page_next);
       }
       more = again;
     }
@@ -571,7 +582,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           const float send = up ? l[k] : l[k + s], keep = up ? l[k + s] : l[k];
           l[k] = keep + __shfl_xor_sync(0xffffffffu, send, s);
         }
-      if (HW < 32) l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
+      l[0] += __shfl_xor_sync(0xffffffffu, l[0], 16);
       if (lane < HW) red[w * HW + lane] = l[0];
       wg_or(wg, false);
       const int64_t part = 2 * unit + (j0 > 0 ? 0 : 1);  // of the workspace arrays
@@ -660,8 +671,9 @@ dsa_status launch(const CUtensorMap &kv_map, const void *q, const PagedAttnParam
   if (st != DSA_OK) return st;
   cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
   if (e != cudaSuccess) return cuda_fail(e);
-  paged_attn_kernel<C><<<static_cast<unsigned>(P.units * P.groups), C::kThreads, C::kSmemBytes, stream>>>(q_map, kv_map, P);
-  return check_launch();
+  e = launch_overlapped(paged_attn_kernel<C>, dim3(static_cast<unsigned>(P.units * P.groups)), C::kThreads, C::kSmemBytes,
+                        stream, q_map, kv_map, P);
+  return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
 }  // namespace

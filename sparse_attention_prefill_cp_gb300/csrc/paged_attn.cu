@@ -66,7 +66,7 @@ struct PagedCfg {
   static constexpr int kOffBar = kOffStat + WG * kStatWg * 4;
   static constexpr int kNumBars = 2 + 2 * NT + 2 * NR + 2 + 2 + 1 + 1;
   static constexpr int kOffMisc = kOffBar + (kNumBars + 1) / 2 * 16;
-  // [0] tmem, [1] failed wait, [2..3] bad index, [4] first query, [5] its first block, [8..8+2*kWarps) scan
+  // [0] tmem, [1] failed wait, [2..3] bad index, [4] first query, [5] where in it, [8..8+2*kWarps) scan
   static constexpr int kSmemBytes = kOffMisc + (8 + 2 * kWarps) * 4 + 1024;
   static constexpr uint32_t kIdescQK = idesc_bf16(kRows, HP, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16(128, HP, true, true);
@@ -98,26 +98,34 @@ __device__ __forceinline__ bool wg_or(int wg, bool p) {
 }
 
 // A unit's walk through its share: segments of consecutive blocks of one query.
+// A query counts a block more than it has, its first: what a segment costs beside
+// its blocks (Q, the first block's maxima, the result) is about a block's time, so
+// units of many short queries get fewer blocks (64 queries of 1 to 16 blocks and
+// 128 heads: 49 -> 37 us).
 struct Walk {
   int q, j0, j1, nb, len, row;  // query, blocks [j0, j1) of its nb, positions it sees, its row of the table
-  int64_t left;                 // blocks of the share from j0 on
-  // the segment at block j of query `query`; false: the share is done
-  __device__ __forceinline__ bool start(const PagedAttnParams &P, int query, int j) {
-    if (left <= 0) return false;
-    for (q = query; q < P.n; ++q, j = 0) {
+  int take;                     // what the segment counts
+  int64_t left;                 // of the share from here on
+  // the segment at count `o` of query `query`; false: the share is done
+  __device__ __forceinline__ bool start(const PagedAttnParams &P, int query, int o) {
+    for (q = query; q < P.n && left > 0; ++q, o = 0) {
       len = __ldg(P.lens + q);
       nb = paged_blocks(len, P.nsel, P.max_pages, P.page_shift);
-      if (nb > j) break;
+      if (nb == 0) continue;
+      take = static_cast<int>(min(static_cast<int64_t>(nb + 1 - o), left));
+      j0 = max(o - 1, 0);
+      j1 = o + take - 1;
+      if (j1 > j0) {
+        row = P.req ? __ldg(P.req + q) : q;
+        if (row < 0 || row >= P.batch) len = 0;  // reported by the loading warp
+        return true;
+      }
+      left -= take;  // the share ends with the query's extra count
     }
-    if (q >= P.n) return false;
-    row = P.req ? __ldg(P.req + q) : q;
-    if (row < 0 || row >= P.batch) len = 0;  // reported by the loading warp
-    j0 = j;
-    j1 = static_cast<int>(min(static_cast<int64_t>(nb), j + left));
-    return true;
+    return false;
   }
   __device__ __forceinline__ bool next(const PagedAttnParams &P) {
-    left -= j1 - j0;
+    left -= take;
     return start(P, q + 1, 0);
   }
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nb; }
@@ -195,12 +203,16 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     tma_prefetch_desc(&kv_map);
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before may still run
-  // Where the share starts: the threads sum consecutive queries' blocks, and the
-  // one that holds the share's first block finds its query.
+  // Where the share starts: the threads sum what consecutive queries count, and
+  // the one that holds the share's first count finds its query.
   const int per = (P.n + C::kThreads - 1) / C::kThreads;
   const int i0 = min(tid * per, P.n), i1 = min(i0 + per, P.n);
   int64_t mine = 0;
-  for (int i = i0; i < i1; ++i) mine += paged_blocks(__ldg(P.lens + i), P.nsel, P.max_pages, P.page_shift);
+  auto counts = [&](int i) {
+    const int nb = paged_blocks(__ldg(P.lens + i), P.nsel, P.max_pages, P.page_shift);
+    return nb ? nb + 1 : 0;
+  };
+  for (int i = i0; i < i1; ++i) mine += counts(i);
   int64_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -222,13 +234,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   if (g0 < g1 && g0 >= before && g0 < before + mine) {
     int64_t at = before;
     for (int i = i0; i < i1; ++i) {
-      const int nb = paged_blocks(__ldg(P.lens + i), P.nsel, P.max_pages, P.page_shift);
-      if (g0 < at + nb) {
+      const int c = counts(i);
+      if (g0 < at + c) {
         misc[4] = i;
         misc[5] = static_cast<int>(g0 - at);
         break;
       }
-      at += nb;
+      at += c;
     }
   }
   __syncthreads();
@@ -257,7 +269,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           bad[1] = walk.q;
         }
         // it ends in a later unit: the share's last segment
-        if (walk.j1 < walk.nb) join = make_int2(walk.q, static_cast<int>((g1 - walk.left + walk.nb - 1) / share));
+        if (walk.j1 < walk.nb) join = make_int2(walk.q, static_cast<int>((g1 - walk.left + walk.take + walk.nb - 1 - walk.j1) / share));
       }
       if (seg > 0) ok = __all_sync(0xffffffffu, wait_for(q_free, (seg - 1) & 1, failed, 80, walk.q));
       if (!ok) break;
@@ -552,13 +564,14 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           *reinterpret_cast<uint4 *>(prow + ((u ^ (r & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
         }
         if (!used) {
-          // zero the row in this warpgroup's share of the block's value tiles: what is there may be NaN
+          // zero the row in this warpgroup's share of the block's value tiles: what is there may be NaN (a lane's units
+          // in its own order, so that eight rows fall on eight bank groups: 1 against 8 K cycles a block)
 #pragma unroll 1
           for (int o = wg; o < kTiles; o += C::WG) {
             uint8_t *row = smem + C::kOffTiles + (kTiles * blk + o) % C::NT * kTileBytes + r * 128;
 #pragma unroll
             for (int u = 0; u < 16; ++u)
-              *reinterpret_cast<uint4 *>(row + (u >> 3) * kChunkBytes + ((u & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4 *>(row + (u >> 3) * kChunkBytes + (((u ^ r) & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
           }
         }
         tc_fence_before();

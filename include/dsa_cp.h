@@ -771,7 +771,7 @@ dsa_status dsa_poll_device_error(dsa_stream_t stream);
  * bounds checks around the paged cache (52 a length, 53 a released page, 54 free
  * pages, 55 slots, 56 a written slot, 57 a page number, 58 a query's request or
  * length; the detail is the request, the row or the query), 80-92 waits of the
- * attention over it, 93 of the block selection. */
+ * attention over it, 93-96 of the block selection. */
 dsa_status dsa_poll_device_error_detail(dsa_stream_t stream, int32_t *detail);
 
 /* Static string for a status code. */

@@ -8,10 +8,16 @@
 // One CTA takes the queries of a group (four that share a request, or one), 128
 // pages at a time: pages as the M = 128 side of the MMA, (query, head) pairs as
 // N = 64 each, K = 128, so a page is a TMEM lane and the weighted sum over heads
-// is a thread's own loop.  The mean keys of a tile are gathered by cp.async while
-// the MMA of the tile before runs and the one before that is summed.  Scores stay
-// in shared memory as order-preserving integers; the k-th largest is found bit by
-// bit from the counts, and one pass in page order writes the list.
+// is a thread's own loop.  Warps: sums, a warpgroup for each of four queries or two
+// that take the tiles of one by turns; MMA issue; four that gather the mean keys
+// by cp.async into a ring of tiles, page numbers a tile ahead.  Scores stay
+// in shared memory as order-preserving integers, from where a team of the warps of
+// a query takes its keys into registers, finds the cut bit by bit from counts (the
+// search ends as soon as a count fits) and writes the list in page order.
+//
+// What bounds it: a group of four queries and 1,024 pages takes 8 x 1,024 cycles
+// of MMA; gathering a tile and summing one take about as long, and the start and
+// the choice of a CTA, one to an SM, run alone.
 #include "attn_common.cuh"
 #include "internal.h"
 
@@ -20,7 +26,7 @@ namespace {
 
 constexpr int kHI = 64, kDI = 128;
 constexpr int kRows = 128;                  // pages per tile
-constexpr int kThreads = 256;
+constexpr int kLoadWarps = 4;
 constexpr int kChunkBytes = kRows * 128;    // 64 of the 128 dims (128B swizzle)
 constexpr int kTileBytes = 2 * kChunkBytes;
 
@@ -38,14 +44,20 @@ template <int QT_>
 struct SelCfg {
   static constexpr int QT = QT_;  // queries of a group
   static constexpr int N = QT * kHI;
-  static constexpr int kOffQ = 2 * kTileBytes;
+  static constexpr int kStages = QT == 1 ? 2 : 3;   // tiles in the ring (one query: two CTAs fit an SM)
+  static constexpr int kBufs = 2;                   // accumulators
+  static constexpr int kSumWarps = QT == 1 ? 8 : 16, kTeamWarps = kSumWarps / QT;
+  static constexpr int kMmaWarp = kSumWarps, kFirstLoadWarp = kMmaWarp + 1;
+  static constexpr int kThreads = 32 * (kFirstLoadWarp + kLoadWarps);
+  static constexpr int kOffQ = kStages * kTileBytes;
   static constexpr int kQChunk = N * 128;
   static constexpr int kOffW = kOffQ + 2 * kQChunk;
   static constexpr int kOffBar = kOffW + QT * kHI * 4;
-  // [0] tmem, [1] failed, [2..3] bad, [4..7] request, [8..11] pages, [16..31] counts
-  static constexpr int kOffMisc = kOffBar + 16;
-  static constexpr int kOffKeys = kOffMisc + 128;  // uint32 [QT][max_pages, to whole tiles]
-  static constexpr int kTmemCols = 2 * N;
+  static constexpr int kNumBars = 2 * kStages + 2 * kBufs;
+  // [0] tmem, [1] failed, [2..3] bad, [4..7] request, [8..11] pages, [16..47] counts
+  static constexpr int kOffMisc = kOffBar + (kNumBars + 1) / 2 * 16;
+  static constexpr int kOffKeys = kOffMisc + 192;   // uint32 [QT][max_pages, to whole tiles]
+  static constexpr int kTmemCols = kBufs * N;
   static constexpr uint32_t kIdesc = idesc_bf16(kRows, N, false, false);
 };
 
@@ -58,12 +70,133 @@ __device__ __forceinline__ uint32_t ordered(float s) {
   return max(k, 2u);
 }
 
+// Barrier among the warps of a team.
+template <int W>
+__device__ __forceinline__ void team_sync(int team) {
+  if (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(W * 32) : "memory");
+}
+
+// The choice of one query by a team of W warps; `team` numbers the barrier, w the
+// warp.  Warp w holds keys [w * per, w * per + per) of kq, a lane every 32nd.
+template <int W>
+__device__ __forceinline__ void choose(const uint32_t *kq, int have, int nsel, int team, int w, int lane, int32_t *counts,
+                                       int32_t *out) {
+  constexpr int kHeld = 8;  // keys a lane keeps in registers
+  if (have <= nsel) {
+    for (int k = w * 32 + lane; k < nsel; k += W * 32) out[k] = k < have ? k : -1;
+    return;
+  }
+  const int per = (have + 32 * W - 1) / (32 * W) * 32, first = w * per, rounds = per / 32;
+  uint32_t v[kHeld];
+  auto take = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      const int b = first + (k0 + k) * 32 + lane;
+      v[k] = k0 + k < rounds && b < have ? kq[b] : 0u;  // no key is 0
+    }
+  };
+  take(0);
+  // how many keys of the team reach c; two sets of counts by turns, so that one barrier a count is enough
+  int turn = 0;
+  auto reach = [&](uint32_t c) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) n += v[k] >= c;
+    for (int k0 = kHeld; k0 < rounds; k0 += kHeld) {
+      uint32_t x[kHeld];
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        const int b = first + (k0 + k) * 32 + lane;
+        x[k] = k0 + k < rounds && b < have ? kq[b] : 0u;
+      }
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) n += x[k] >= c;
+    }
+    n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
+    if (W == 1) return n;
+    int32_t *set = counts + turn * 16 + team * W;
+    turn ^= 1;
+    if (lane == 0) set[w] = n;
+    team_sync<W>(team);
+    n = 0;
+#pragma unroll
+    for (int k = 0; k < W; ++k) n += set[k];
+    return n;
+  };
+  // the largest cut that at least nsel keys reach, or any that exactly nsel reach
+  uint32_t cut = 0;
+  int n = have;
+  for (int bit = 31; bit >= 0 && n != nsel; --bit) {
+    const uint32_t c = cut | 1u << bit;
+    const int m = reach(c);
+    if (m >= nsel) {
+      cut = c;
+      n = m;
+    }
+  }
+  // keys above the cut are all taken; of those equal to it the first `ties`
+  int above = 0, equal = 0;
+  auto tally = [&](uint32_t key) {
+    above += key > cut;
+    equal += key == cut;
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) tally(v[k]);
+  for (int k = kHeld; k < rounds; ++k) {
+    const int b = first + k * 32 + lane;
+    tally(b < have ? kq[b] : 0u);
+  }
+  above = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(above)));
+  equal = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(equal)));
+  int at = 0, tied = 0, ties = nsel;  // list entries and ties of the warps before; ties to take
+  if (W > 1) {
+    team_sync<W>(team);  // the last counts have been read
+    int32_t *set = counts + team * W;
+    if (lane == 0) {
+      set[w] = above;
+      set[16 + w] = equal;
+    }
+    team_sync<W>(team);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      ties -= set[k];
+      if (k < w) {
+        at += set[k];
+        tied += set[16 + k];
+      }
+    }
+  } else {
+    ties -= above;
+  }
+  at += min(tied, ties);
+  ties = max(ties - tied, 0);
+  const uint32_t below = (1u << lane) - 1u;
+  auto write = [&](uint32_t key, int b) {
+    const uint32_t same = __ballot_sync(0xffffffffu, key == cut);
+    const bool took = key > cut || (key == cut && __popc(same & below) < ties);
+    const uint32_t taken = __ballot_sync(0xffffffffu, took);
+    if (took) out[at + __popc(taken & below)] = b;
+    at += __popc(taken);
+    ties -= min(ties, __popc(same));
+  };
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k)
+    if (k < rounds) write(v[k], first + k * 32 + lane);
+  for (int k = kHeld; k < rounds; ++k) {
+    const int b = first + k * 32 + lane;
+    write(b < have ? kq[b] : 0u, b);
+  }
+}
+
 template <class C>
-__global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectParams P) {
+__global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectParams P) {
   constexpr int QT = C::QT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t *done = reinterpret_cast<uint64_t *>(smem + C::kOffBar);  // [2] MMA of a tile done
+  uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + C::kOffBar);  // [kStages] a tile's keys are there (load warps)
+  uint64_t *k_free = k_full + C::kStages;                              // [kStages] its MMA is done (commit)
+  uint64_t *a_full = k_free + C::kStages;                              // [kBufs] an accumulator is complete (commit)
+  uint64_t *a_free = a_full + C::kBufs;                                // [kBufs] it has been read (sum warps)
   int32_t *misc = reinterpret_cast<int32_t *>(smem + C::kOffMisc);
   int32_t *failed = misc + 1, *bad = misc + 2;
   float *ws = reinterpret_cast<float *>(smem + C::kOffW);
@@ -74,17 +207,34 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
 
   if (tid == 0) {
     misc[1] = misc[2] = misc[3] = 0;
-    mbar_init(&done[0], 1);
-    mbar_init(&done[1], 1);
+    for (int s = 0; s < C::kStages; ++s) {
+      mbar_init(&k_full[s], kLoadWarps);
+      mbar_init(&k_free[s], 1);
+    }
+    for (int b = 0; b < C::kBufs; ++b) {
+      mbar_init(&a_full[b], 1);
+      mbar_init(&a_free[b], QT == 1 ? 4 : C::kSumWarps);
+    }
     fence_mbar_init();
   }
-  if (warp == 0) {
+  if (warp == C::kMmaWarp) {
     tmem_alloc(reinterpret_cast<uint32_t *>(&misc[0]), C::kTmemCols);
     tmem_relinquish();
   }
-  if (tid < QT) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before may still run
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // Q: rows (query, head) of 256 bytes, 16-byte unit u of a 128-byte half at u ^ (row & 7); heads behind HI are zero
+  for (int x = tid; x < C::N * 16; x += C::kThreads) {
+    const int r = x >> 4, u = x & 15, i = i0 + (r >> 6), h = r & 63;
+    const bool there = i < P.n && h < P.HI;
+    const uint4 *src = P.q + (static_cast<int64_t>(there ? i : 0) * P.HI + (there ? h : 0)) * (kDI / 8) + u;
+    cp_async_16(smem_u32(smem + C::kOffQ) + (u >> 3) * C::kQChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4), src,
+                there ? 16u : 0u);
+  }
+  cp_async_commit();
+  if (warp == C::kFirstLoadWarp && lane < QT) {
     // a query's request and how many pages it sees (no query, or a bad request: none)
-    const int i = i0 + tid;
+    const int i = i0 + lane;
     int row = -1, have = 0;
     if (i < P.n) {
       row = P.req ? P.req[i] : i;
@@ -94,178 +244,171 @@ __global__ void __launch_bounds__(kThreads) block_select_kernel(const SelectPara
         record_error(P.err, DSA_ERR_DEVICE_BOUNDS, 58, i);
       if (row < 0 || row >= P.batch) have = 0;
     }
-    misc[4 + tid] = row;
-    misc[8 + tid] = have;
+    misc[4 + lane] = row;
+    misc[8 + lane] = have;
   }
-  // Q: rows (query, head) of 256 bytes, 16-byte unit u of a 128-byte half at u ^ (row & 7); heads behind HI are zero
-#pragma unroll 1
-  for (int x = tid; x < C::N * 16; x += kThreads) {
-    const int r = x >> 4, u = x & 15, i = i0 + (r >> 6), h = r & 63;
-    const bool there = i < P.n && h < P.HI;
-    const uint4 *src = P.q + (static_cast<int64_t>(there ? i : 0) * P.HI + (there ? h : 0)) * (kDI / 8) + u;
-    cp_async_16(smem_u32(smem + C::kOffQ) + (u >> 3) * C::kQChunk + r * 128 + (((u & 7) ^ (r & 7)) << 4), src,
-                there ? 16u : 0u);
-  }
-  for (int x = tid; x < QT * kHI; x += kThreads) {
+  for (int x = tid; x < QT * kHI; x += C::kThreads) {
     const int i = i0 + x / kHI, h = x % kHI;
     ws[x] = i < P.n && h < P.HI ? P.w[static_cast<int64_t>(i) * P.HI + h] : 0.f;
   }
+  cp_async_wait<0>();
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = static_cast<uint32_t>(misc[0]);
-  const uint64_t a0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSW128);
-  const uint64_t b0 = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024, kLayoutSW128);
 
-  int tile = 0;  // MMAs issued so far: buffer tile & 1, phase tile >> 1
-  bool ok = true;
-  // runs of queries with the same request: usually one
-  for (int q0 = 0; ok && q0 < QT;) {
+  // Runs of queries with the same request (usually one): [q0, q1), the pages and the tiles that one of them has to
+  // choose from; tiles are numbered through.
+  struct Run {
+    int q0, q1, pages, tiles;
+    const int32_t *row;
+  };
+  auto run_at = [&](int q0) {
+    Run r;
     const int row = misc[4 + q0];
-    int q1 = q0 + 1, pages = misc[8 + q0];
-    while (q1 < QT && misc[4 + q1] == row) pages = max(pages, misc[8 + q1++]);
-    const int32_t *trow = P.table + static_cast<int64_t>(max(row, 0)) * P.max_pages;
-    bool any = false;  // a query that has to choose
-    for (int q = q0; q < q1; ++q) any |= misc[8 + q] > P.nsel;
-    const int tiles = any ? (pages + kRows - 1) / kRows : 0;
-    auto load = [&](int t, int buf) {
-      // a page's key: 16 units by 16 lanes
-#pragma unroll
-      for (int x = 0; x < kRows * 16 / kThreads; ++x) {
-        const int r = x * (kThreads / 16) + (tid >> 4), u = tid & 15, b = t * kRows + r;
-        const int page = b < pages ? __ldg(trow + b) : -1;
-        const bool there = page >= 0 && page < P.num_pages;
-        cp_async_16(smem_u32(smem) + buf * kTileBytes + (u >> 3) * kChunkBytes + r * 128 + (((u & 7) ^ (r & 7)) << 4),
-                    P.keys + static_cast<int64_t>(there ? page : 0) * (kDI / 8) + u, there ? 16u : 0u);
-      }
-      cp_async_commit();
+    r.q0 = q0;
+    r.q1 = q0 + 1;
+    r.pages = misc[8 + q0];
+    while (r.q1 < QT && misc[4 + r.q1] == row) r.pages = max(r.pages, misc[8 + r.q1++]);
+    r.row = P.table + static_cast<int64_t>(max(row, 0)) * P.max_pages;
+    bool any = false;
+    for (int q = r.q0; q < r.q1; ++q) any |= misc[8 + q] > P.nsel;
+    r.tiles = any ? (r.pages + kRows - 1) / kRows : 0;
+    return r;
+  };
+  bool ok = true;
+  int tile = 0;
+  if (warp >= C::kFirstLoadWarp) {
+    // ---------------- gather: warp w takes rows 8x + 2w + {0, 1} of a tile, x = 0..15, sixteen lanes a row; lane l
+    // knows the page of row 8 (l / 2) + 2w + l % 2.  A tile is handed on when the next one's copies are on their way.
+    const int w = warp - C::kFirstLoadWarp, u = lane & 15, my_row = 8 * (lane >> 1) + 2 * w + (lane & 1);
+    const uint32_t to = smem_u32(smem) + (u >> 3) * kChunkBytes;
+    auto land = [&](int t) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[t % C::kStages]);
     };
-    // the scores of tile t, whose MMA was the n-th
-    auto sum = [&](int t, int n) {
-      const int b = t * kRows + (warp & 3) * 32 + lane;
-      const int page = b < pages ? __ldg(trow + b) : 0;
-      const bool there = page >= 0 && page < P.num_pages;
-      ok = __all_sync(0xffffffffu, ok && wait_for(&done[n & 1], (n >> 1) & 1, failed, 93, t));
-      if (!ok) return;
-      tc_fence_after();
-      // the two warpgroups take alternate queries, or alternate tiles where there is one query
-      for (int q = QT > 1 ? warp >> 2 : 0; q < QT; q += QT > 1 ? 2 : 1) {
-        if (QT == 1 ? (t & 1) != (warp >> 2) : q < q0 || q >= q1) continue;
-        const uint32_t at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (n & 1) * C::N + q * kHI;
-        float s[2] = {0.f, 0.f};
+    for (int q0 = 0; ok && q0 < QT;) {
+      const Run r = run_at(q0);
+      auto lookup = [&](int t) {
+        const int b = t * kRows + my_row;
+        return t < r.tiles && b < r.pages ? r.row[b] : -1;
+      };
+      int next = lookup(0);
+      for (int t = 0; t < r.tiles; ++t, ++tile) {
+        const int page = next >= 0 && next < P.num_pages ? next : -1;
+        next = lookup(t + 1);
+        const int s = tile % C::kStages;
+        ok = __all_sync(0xffffffffu, wait_for(&k_free[s], ((tile / C::kStages) & 1) ^ 1, failed, 93, tile));
+        if (!ok) break;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x[32];
-          tmem_ld32(at + 32 * half, x);
-          tmem_ld_wait();
-          const float *wq = ws + q * kHI + 32 * half;
-#pragma unroll
-          for (int k = 0; k < 32; k += 4) {
-            const float4 w4 = *reinterpret_cast<const float4 *>(wq + k);
-            s[0] += w4.x * fmaxf(__uint_as_float(x[k]), 0.f);
-            s[1] += w4.y * fmaxf(__uint_as_float(x[k + 1]), 0.f);
-            s[0] += w4.z * fmaxf(__uint_as_float(x[k + 2]), 0.f);
-            s[1] += w4.w * fmaxf(__uint_as_float(x[k + 3]), 0.f);
-          }
+        for (int x = 0; x < 16; ++x) {
+          const int row = 8 * x + 2 * w + (lane >> 4), pg = __shfl_sync(0xffffffffu, page, 2 * x + (lane >> 4));
+          cp_async_16(to + s * kTileBytes + row * 128 + (((u & 7) ^ (row & 7)) << 4),
+                      P.keys + static_cast<int64_t>(max(pg, 0)) * (kDI / 8) + u, pg >= 0 ? 16u : 0u);
         }
-        const int have = misc[8 + q];
-        uint32_t key = ordered(s[0] + s[1]);
-        if (!there) {
-          key = 1u;
-          if (b < have) {
+        cp_async_commit();
+        if (tile > 0) {
+          cp_async_wait<1>();
+          land(tile - 1);
+        }
+      }
+      q0 = r.q1;
+    }
+    cp_async_wait<0>();
+    if (ok && tile > 0) land(tile - 1);
+  } else if (warp == C::kMmaWarp) {
+    // ---------------- MMA issue: the whole warp runs the loop, one elected lane issues
+    const bool issuer = elect_one();
+    const uint64_t a0 = smem_desc(smem_u32(smem), 16, 1024, kLayoutSW128);
+    const uint64_t b0 = smem_desc(smem_u32(smem + C::kOffQ), 16, 1024, kLayoutSW128);
+    for (int q0 = 0; ok && q0 < QT;) {
+      const Run r = run_at(q0);
+      for (int t = 0; t < r.tiles; ++t, ++tile) {
+        const int s = tile % C::kStages, buf = tile % C::kBufs;
+        ok = __all_sync(0xffffffffu, wait_for(&k_full[s], (tile / C::kStages) & 1, failed, 94, tile) &&
+                                         wait_for(&a_free[buf], ((tile / C::kBufs) & 1) ^ 1, failed, 95, tile));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t a = desc_add(a0, static_cast<uint32_t>(s * kTileBytes) >> 4);
+        if (issuer) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ss(tmem + buf * C::N, desc_add(a, (k >> 2) * (kChunkBytes >> 4) + (k & 3) * 2),
+                   desc_add(b0, (k >> 2) * (C::kQChunk >> 4) + (k & 3) * 2), C::kIdesc, k > 0 ? 1u : 0u);
+          mma_commit(&k_free[s]);
+          mma_commit(&a_full[buf]);
+        }
+        __syncwarp();
+      }
+      q0 = r.q1;
+    }
+  } else {
+    // ---------------- sums: a warpgroup a query of a group, or every second tile of one query
+    const int wg = warp >> 2, q = QT == 1 ? 0 : wg;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + q * kHI;
+    const float *wq = ws + q * kHI;
+    const int have = misc[8 + q];
+    for (int q0 = 0; ok && q0 < QT;) {
+      const Run r = run_at(q0);
+      for (int t = 0; t < r.tiles; ++t, ++tile) {
+        if (QT == 1 && tile % C::kBufs != wg) continue;
+        const int buf = tile % C::kBufs, b = t * kRows + (warp & 3) * 32 + lane;
+        const bool mine = q >= r.q0 && q < r.q1;
+        const int page = mine && b < have ? r.row[b] : 0;
+        ok = __all_sync(0xffffffffu, wait_for(&a_full[buf], (tile / C::kBufs) & 1, failed, 96, tile));
+        if (!ok) break;
+        tc_fence_after();
+        if (mine) {
+          uint64_t s[2] = {0, 0};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t x[32];
+            tmem_ld32(lane_base + buf * C::N + 32 * half, x);
+            tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              const float4 w4 = *reinterpret_cast<const float4 *>(wq + 32 * half + k);
+              s[0] = f2_fma(f2_pack(w4.x, w4.y),
+                            f2_pack(fmaxf(__uint_as_float(x[k]), 0.f), fmaxf(__uint_as_float(x[k + 1]), 0.f)), s[0]);
+              s[1] = f2_fma(f2_pack(w4.z, w4.w),
+                            f2_pack(fmaxf(__uint_as_float(x[k + 2]), 0.f), fmaxf(__uint_as_float(x[k + 3]), 0.f)), s[1]);
+            }
+          }
+          float s0, s1, s2, s3;
+          f2_unpack(s[0], s0, s1);
+          f2_unpack(s[1], s2, s3);
+          uint32_t key = ordered((s0 + s1) + (s2 + s3));
+          if (page < 0 || page >= P.num_pages) {
+            key = 1u;
             bad[0] = 57;
             bad[1] = i0 + q;
           }
+          if (b < P.keep_first || b >= have - P.keep_last) key = 0xffffffffu;
+          keys[q * ld + b] = key;
         }
-        if (b < P.keep_first || b >= have - P.keep_last) key = 0xffffffffu;
-        keys[q * ld + b] = b < have ? key : 0u;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&a_free[buf]);
       }
-      tc_fence_before();
-    };
-    if (tiles > 0) load(0, tile & 1);
-    for (int t = 0; t < tiles; ++t, ++tile) {
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      tc_fence_before();
-      // tile t is there; the accumulator of tile t - 2 has been read.  All threads leave together after a failed wait
-      if (__syncthreads_or(!ok)) break;
-      tc_fence_after();
-      if (tid == 0) {
-        const uint64_t a = desc_add(a0, static_cast<uint32_t>((tile & 1) * kTileBytes) >> 4);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_ss(tmem + (tile & 1) * C::N, desc_add(a, (k >> 2) * (kChunkBytes >> 4) + (k & 3) * 2),
-                 desc_add(b0, (k >> 2) * (C::kQChunk >> 4) + (k & 3) * 2), C::kIdesc, k > 0 ? 1u : 0u);
-        mma_commit(&done[tile & 1]);
-      }
-      __syncwarp();
-      if (t > 0)  // the MMA before has read the other buffer
-        ok = __all_sync(0xffffffffu, wait_for(&done[(tile - 1) & 1], ((tile - 1) >> 1) & 1, failed, 93, t));
-      if (ok && t + 1 < tiles) load(t + 1, (tile + 1) & 1);
-      if (t > 0) sum(t - 1, tile - 1);
-    }
-    if (ok && tiles > 0) sum(tiles - 1, tile - 1);
-    cp_async_wait<0>();
-    tc_fence_before();
-    ok = !__syncthreads_or(!ok);
-    tc_fence_after();
-    q0 = q1;
-  }
-
-  // ---------------- the choice: a team of warps per query
-  constexpr int kTeamWarps = 8 / QT;
-  const int q = warp / kTeamWarps, i = i0 + q, member = tid - q * kTeamWarps * 32;
-  const int have = misc[8 + q];
-  if (ok && i < P.n && P.lens[i] >= 0) {
-    int32_t *out = P.out + static_cast<int64_t>(i) * P.nsel;
-    if (have <= P.nsel) {
-      for (int k = member; k < P.nsel; k += kTeamWarps * 32) out[k] = k < have ? k : -1;
-    } else {
-      const uint32_t *kq = keys + q * ld;
-      int32_t *count = misc + 16;  // [2][8]: partial counts, two sets by turns
-      auto team_sum = [&](int c, int turn) {
-        c = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(c)));
-        if (kTeamWarps == 1) return c;
-        if (lane == 0) count[(turn & 1) * 8 + warp] = c;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + q), "r"(kTeamWarps * 32) : "memory");
-        int s = 0;
-#pragma unroll
-        for (int k = 0; k < kTeamWarps; ++k) s += count[(turn & 1) * 8 + q * kTeamWarps + k];
-        return s;
-      };
-      uint32_t cut = 0;  // the largest value that at least nsel keys reach
-      for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t c = cut | 1u << bit;
-        int n = 0;
-        for (int b = member; b < have; b += kTeamWarps * 32) n += kq[b] >= c;
-        if (team_sum(n, bit) >= P.nsel) cut = c;
-      }
-      int above = 0;
-      for (int b = member; b < have; b += kTeamWarps * 32) above += kq[b] > cut;
-      int ties = P.nsel - team_sum(above, 1);  // of the keys equal to the cut, the first so many
-      if (member < 32) {
-        int at = 0;
-        for (int b0 = 0; b0 < have && at < P.nsel; b0 += 32) {
-          const uint32_t key = b0 + lane < have ? kq[b0 + lane] : 0u;
-          const uint32_t same = __ballot_sync(0xffffffffu, key == cut && b0 + lane < have);
-          const uint32_t below = (1u << lane) - 1u;
-          const bool take = key > cut || ((same >> lane) & 1u && __popc(same & below) < ties);
-          const uint32_t taken = __ballot_sync(0xffffffffu, take);
-          if (take) out[at + __popc(taken & below)] = b0 + lane;
-          at += __popc(taken);
-          ties -= min(ties, __popc(same));
-        }
-      }
+      q0 = r.q1;
     }
   }
   tc_fence_before();
-  __syncthreads();
-  if (tid == 0 && *failed) record_error(P.err, DSA_ERR_DEVICE_TIMEOUT, *failed >> 24, *failed & 0xffffff);
-  if (tid == 0 && bad[0]) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, bad[0], bad[1]);
-  if (warp == 0) {
+  ok = !__syncthreads_or(!ok);
+  if (warp == C::kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  if (warp < C::kSumWarps && ok) {
+    const int q = warp / C::kTeamWarps, i = i0 + q;
+    if (i < P.n && P.lens[i] >= 0)
+      choose<C::kTeamWarps>(keys + q * ld, misc[8 + q], P.nsel, q, warp % C::kTeamWarps, lane, misc + 16,
+                            P.out + static_cast<int64_t>(i) * P.nsel);
+  }
+  if (tid == 0 && *failed) record_error(P.err, DSA_ERR_DEVICE_TIMEOUT, *failed >> 24, *failed & 0xffffff);
+  if (tid == 0 && bad[0]) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, bad[0], bad[1]);
 }
 
 template <class C>
@@ -281,8 +424,9 @@ dsa_status launch(const SelectParams &P, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(block_select_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(kMaxSmem));
   if (e != cudaSuccess) return cuda_fail(e);
-  block_select_kernel<C><<<static_cast<unsigned>((P.n + C::QT - 1) / C::QT), kThreads, bytes, stream>>>(P);
-  return check_launch();
+  e = launch_overlapped(block_select_kernel<C>, dim3(static_cast<unsigned>((P.n + C::QT - 1) / C::QT)), C::kThreads, bytes,
+                        stream, P);
+  return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }
 
 }  // namespace

@@ -819,32 +819,47 @@ def _page_size(P: int) -> int:
     return int(P)
 
 
-def _need_table(page_table: torch.Tensor) -> tuple[int, int]:
-    _need(page_table, torch.int32, "page_table")
-    if page_table.dim() != 2 or page_table.shape[1] < 1:
-        raise ValueError("page_table must be [batch, max_pages]")
-    _int32(table_entries=page_table.numel())
-    return tuple(page_table.shape)
+_INT32_MAX = 0x7fffffff
 
 
-def _need_ints(t: torch.Tensor | None, n: int, name: str) -> None:
-    if t is not None:
+def _shape(t: torch.Tensor, dtype: torch.dtype, dims: int, name: str, form: str) -> torch.Size:
+    """The shape of a contiguous CUDA tensor of that type and number of dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name)
+    s = t.shape
+    if len(s) != dims:
+        raise ValueError(f"{name} must be {form}")
+    return s
+
+
+def _need_table(page_table: torch.Tensor) -> torch.Size:
+    s = _shape(page_table, torch.int32, 2, "page_table", "[batch, max_pages]")
+    if s[1] < 1 or s[0] * s[1] > _INT32_MAX:
+        raise ValueError("page_table must be [batch, max_pages] with a page at least and fewer than 2^31 entries")
+    return s
+
+
+def _need_ints(t: torch.Tensor, n: int, name: str) -> None:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
         _need(t, torch.int32, name)
-        if tuple(t.shape) != (n,):
-            raise ValueError(f"{name} must be [{n}]")
+    if t.shape != (n,):
+        raise ValueError(f"{name} must be [{n}]")
 
 
 def _pages(t: torch.Tensor, name: str) -> tuple[int, int, int, int, int]:
     """(pages, rows, columns, page stride, row stride) of a bf16 [pages, P, D]
     tensor whose rows are contiguous and start on 16-byte boundaries."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.bfloat16 or t.dim() != 3:
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda or len(t.shape) != 3:
         raise ValueError(f"{name} must be a CUDA bfloat16 tensor [num_pages, page_size, D]")
     R, P, D = t.shape
-    _page_size(P)
-    _int32(rows=R * P)
-    row = t.stride(1)
-    page = t.stride(0) if R > 1 else row * P
-    if t.stride(2) != 1 or row < D or row % 8 or page % 8 or page < (P - 1) * row + D or t.data_ptr() % 16:
+    if P not in PAGE_SIZES:
+        _page_size(P)
+    if R * P > _INT32_MAX:
+        raise ValueError(f"{name} has {R * P} rows, not below 2^31")
+    page, row, one = t.stride()
+    if R < 2:
+        page = row * P
+    if one != 1 or row < D or row % 8 or page % 8 or page < (P - 1) * row + D or t.data_ptr() % 16:
         raise ValueError(f"the rows of {name} must be contiguous, not overlap and start on 16-byte boundaries")
     return R, P, D, page, row
 
@@ -862,14 +877,14 @@ def dsa_pages_update(page_table: torch.Tensor, held_lens: torch.Tensor, seq_lens
     P = _page_size(page_size)
     _need_ints(held_lens, B, "held_lens")
     _need_ints(seq_lens, B, "seq_lens")
-    _need(free_pages, torch.int32, "free_pages")
-    if free_pages.dim() != 1:
-        raise ValueError("free_pages must be [num_pages]")
+    pool, = _shape(free_pages, torch.int32, 1, "free_pages", "[num_pages]")
+    if pool > _INT32_MAX:
+        raise ValueError(f"{pool} pages, not below 2^31")
     _need_ints(free_count, 1, "free_count")
     ctx, st = _launch_on(stream, page_table, held_lens, seq_lens, free_pages, free_count)
     with ctx or _HERE:
-        check(load().dsa_pages_update(_addr(page_table), B, width, _addr(held_lens), _addr(seq_lens), P,
-                                      _addr(free_pages), free_pages.numel(), _addr(free_count), st), "dsa_pages_update")
+        check(load().dsa_pages_update(page_table.data_ptr(), B, width, held_lens.data_ptr(), seq_lens.data_ptr(), P,
+                                      free_pages.data_ptr(), pool, free_count.data_ptr(), st), "dsa_pages_update")
     return page_table
 
 
@@ -880,18 +895,19 @@ def dsa_pages_slots(page_table: torch.Tensor, first: torch.Tensor | None, seq_le
     requests in order, -1 behind the last."""
     B, width = _need_table(page_table)
     P = _page_size(page_size)
-    _need_ints(first, B, "first")
+    if first is not None:
+        _need_ints(first, B, "first")
     _need_ints(seq_lens, B, "seq_lens")
-    if num_slots < 0:
+    if not 0 <= num_slots <= _INT32_MAX:
         raise ValueError(f"num_slots = {num_slots}")
-    _int32(num_slots=num_slots)
-    _need_ints(out, num_slots, "out")
+    if out is not None:
+        _need_ints(out, num_slots, "out")
     ctx, st = _launch_on(stream, page_table, first, seq_lens, out)
     with ctx or _HERE:
         if out is None:
             out = torch.empty(num_slots, dtype=torch.int32, device=page_table.device)
-        check(load().dsa_pages_slots(_addr(page_table), B, width, _addr(first), _addr(seq_lens), P, _addr(out),
-                                     num_slots, st), "dsa_pages_slots")
+        check(load().dsa_pages_slots(page_table.data_ptr(), B, width, _addr(first), seq_lens.data_ptr(), P,
+                                     out.data_ptr(), num_slots, st), "dsa_pages_slots")
     return out
 
 
@@ -905,17 +921,17 @@ def dsa_pages_append(kv: torch.Tensor, k_idx: torch.Tensor | None, slots: torch.
     [num_pages, DI].  Slots of one page stand together, ascending.  The rows
     of kv and of cache may lie apart, each starting on a 16-byte boundary."""
     R, P, D, page, row = _pages(cache, "cache")
-    if not isinstance(kv, torch.Tensor) or not kv.is_cuda or kv.dtype != torch.bfloat16 or kv.dim() != 2 or \
+    if not isinstance(kv, torch.Tensor) or kv.dtype != torch.bfloat16 or not kv.is_cuda or len(kv.shape) != 2 or \
             kv.shape[1] != D:
         raise ValueError(f"kv must be a CUDA bfloat16 tensor [n, {D}]")
     n = kv.shape[0]
-    stride = kv.stride(0) if n > 1 else D
-    if kv.stride(1) != 1 or stride < D or stride % 8 or kv.data_ptr() % 16:
+    stride, one = kv.stride()
+    if n < 2:
+        stride = D
+    if one != 1 or stride < D or stride % 8 or kv.data_ptr() % 16:
         raise ValueError("the rows of kv must be contiguous, not overlap and start on 16-byte boundaries")
-    if D < 8 or D % 8:
-        raise ValueError("D must be a multiple of 8")
-    _int32(n=n)
-    _need(slots, torch.int32, "slots")
+    if D < 8 or D % 8 or n > _INT32_MAX:
+        raise ValueError("D must be a multiple of 8, and n below 2^31")
     _need_ints(slots, n, "slots")
     DI = 8
     if (k_idx is None) != (key_cache is None) or (k_idx is None) != (block_keys is None):
@@ -942,32 +958,29 @@ def dsa_block_select(q_idx: torch.Tensor, w: torch.Tensor, block_keys: torch.Ten
     ``keep_first`` and last ``keep_last`` of its pages are always among them,
     the others by the indexer score of their mean keys.  A query with a
     negative length has no row: ``out`` keeps what is there."""
-    _need(q_idx, torch.bfloat16, "q_idx")
-    _need(w, torch.float32, "w")
-    _need(block_keys, torch.bfloat16, "block_keys")
+    n, HI, DI = _shape(q_idx, torch.bfloat16, 3, "q_idx", "[n, HI, DI]")
+    if _shape(w, torch.float32, 2, "w", "[n, HI]") != (n, HI):
+        raise ValueError(f"w must be [{n}, {HI}]")
+    R, DK = _shape(block_keys, torch.bfloat16, 2, "block_keys", "[num_pages, DI]")
+    if DK != DI:
+        raise ValueError(f"block_keys must be [num_pages, {DI}]")
     B, width = _need_table(page_table)
     P = _page_size(page_size)
-    if q_idx.dim() != 3 or tuple(w.shape) != tuple(q_idx.shape[:2]):
-        raise ValueError("q_idx must be [n, HI, DI] and w [n, HI]")
-    n, HI, DI = q_idx.shape
-    if block_keys.dim() != 2 or block_keys.shape[1] != DI:
-        raise ValueError(f"block_keys must be [num_pages, {DI}]")
-    _need(lens, torch.int32, "lens")
     _need_ints(lens, n, "lens")
-    _need_ints(req, n, "req")
-    if req is None and n > B:
+    if req is not None:
+        _need_ints(req, n, "req")
+    elif n > B:
         raise ValueError("more queries than requests (pass req)")
-    _int32(n=n, rows=block_keys.shape[0] * P, blocks=n * nsel, nsel=nsel, keep_first=keep_first, keep_last=keep_last)
-    if out is not None:
-        _need(out, torch.int32, "out")
-        if tuple(out.shape) != (n, nsel):
-            raise ValueError(f"out must be [{n}, {nsel}]")
+    if R * P > _INT32_MAX or n * max(nsel, 1) > _INT32_MAX or max(HI, nsel, abs(keep_first), abs(keep_last)) > _INT32_MAX:
+        raise ValueError("sizes that are not below 2^31")
+    if out is not None and _shape(out, torch.int32, 2, "out", "[n, nsel]") != (n, nsel):
+        raise ValueError(f"out must be [{n}, {nsel}]")
     ctx, st = _launch_on(stream, q_idx, w, block_keys, page_table, lens, req, out)
     with ctx or _HERE:
         if out is None:
             out = torch.empty((n, max(nsel, 0)), dtype=torch.int32, device=q_idx.device)
         check(load().dsa_block_select(q_idx.data_ptr(), w.data_ptr(), n, HI, DI, block_keys.data_ptr(),
-                                      block_keys.shape[0], P, page_table.data_ptr(), B, width, lens.data_ptr(),
+                                      R, P, page_table.data_ptr(), B, width, lens.data_ptr(),
                                       _addr(req), nsel, keep_first, keep_last, out.data_ptr(), st), "dsa_block_select")
     return out
 
@@ -1000,36 +1013,29 @@ def dsa_paged_attn(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tenso
     leaves the query's rows of ``out`` as they are.  ``workspace``: uint8, at
     least dsa_paged_attn_workspace_size bytes, allocated per call when
     omitted."""
-    _need(q, torch.bfloat16, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [n, H, D]")
-    n, H, D = q.shape
+    n, H, D = _shape(q, torch.bfloat16, 3, "q", "[n, H, D]")
     R, P, Dc, page, row = _pages(cache, "cache")
     if Dc != D:
         raise ValueError("q / cache do not match in D")
     B, width = _need_table(page_table)
-    _need(lens, torch.int32, "lens")
     _need_ints(lens, n, "lens")
-    _need_ints(req, n, "req")
-    if req is None and n > B:
+    if req is not None:
+        _need_ints(req, n, "req")
+    elif n > B:
         raise ValueError("more queries than requests (pass req)")
     nsel = 0
     if blocks is not None:
-        _need(blocks, torch.int32, "blocks")
-        if blocks.dim() != 2 or blocks.shape[0] != n or blocks.shape[1] < 1:
+        rows, nsel = _shape(blocks, torch.int32, 2, "blocks", "[n, nsel]")
+        if rows != n or nsel < 1:
             raise ValueError(f"blocks must be [{n}, nsel]")
-        nsel = blocks.shape[1]
-    if attn_sink is not None:
-        _need(attn_sink, torch.float32, "attn_sink")
-        if tuple(attn_sink.shape) != (H,):
-            raise ValueError(f"attn_sink must be [{H}]")
-    if out is not None:
-        _need(out, torch.bfloat16, "out")
-        if tuple(out.shape) != (n, H, Dv):
-            raise ValueError(f"out must be [{n}, {H}, {Dv}]")
+    if attn_sink is not None and _shape(attn_sink, torch.float32, 1, "attn_sink", "[H]") != (H,):
+        raise ValueError(f"attn_sink must be [{H}]")
+    if out is not None and _shape(out, torch.bfloat16, 3, "out", "[n, H, Dv]") != (n, H, Dv):
+        raise ValueError(f"out must be [{n}, {H}, {Dv}]")
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
-    _int32(n=n, H=H, blocks=n * nsel)
+    if n > _INT32_MAX or H > _INT32_MAX or n * nsel > _INT32_MAX:
+        raise ValueError("sizes that are not below 2^31")
     ctx, st = _launch_on(stream, q, cache, page_table, lens, blocks, req, attn_sink, out, workspace)
     with ctx or _HERE:
         if out is None:

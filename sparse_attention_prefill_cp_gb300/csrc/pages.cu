@@ -239,20 +239,28 @@ __global__ void __launch_bounds__(kAppendWarps * 32) pages_append_kernel(const P
   uint4 *const page_keys = A.keys + (static_cast<int64_t>(page) << A.page_shift) * A.key_units;
   if (lane < A.key_units) page_keys[static_cast<int64_t>(r) * A.key_units + lane] = __ldg(key + lane);
   if (r != P - 1) return;
+  // which of the page's rows, t - (P - 1) .. t, are this call's: all that precede in its list as in the page
+  uint32_t fresh[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int row = 32 * k + lane, tt = t - (P - 1 - row);
+    fresh[k] = __ballot_sync(0xffffffffu, row < P && tt >= 0 && __ldg(A.slots + max(tt, 0)) == slot - (P - 1 - row));
+  }
   const int half = lane >> 4, u = lane & 15;
   float sum[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) sum[k] = 0.f;
   constexpr int kBatch = 8;
-#pragma unroll 1
-  for (int r0 = 0; r0 < P; r0 += 2 * kBatch) {
+#pragma unroll
+  for (int r0 = 0; r0 < 128; r0 += 2 * kBatch) {
+    if (r0 >= P) break;
     uint4 x[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int row = r0 + 2 * k + half, tt = t - (P - 1 - row);
-      const bool fresh = tt >= 0 && __ldg(A.slots + tt) == slot - (P - 1 - row);
-      const uint4 *from = fresh ? A.k_idx + static_cast<int64_t>(tt) * A.key_units
-                                : page_keys + static_cast<int64_t>(row) * A.key_units;
+      const int row = r0 + 2 * k + half;
+      const uint4 *from = (fresh[r0 >> 5] >> (row & 31)) & 1u
+                              ? A.k_idx + static_cast<int64_t>(t - (P - 1 - row)) * A.key_units
+                              : page_keys + static_cast<int64_t>(row) * A.key_units;
       x[k] = u < A.key_units ? from[u] : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll

@@ -762,6 +762,6 @@ extern "C" dsa_status dsa_paged_attn(const void *q, int32_t n, const void *cache
   st = div.group_heads == 16   ? launch<Cfg16>(kv_map, q, P, s)
        : div.group_heads == 32 ? launch<Cfg32>(kv_map, q, P, s)
                                : launch<Cfg64>(kv_map, q, P, s);
-  if (st != DSA_OK) return st;
+  if (st != DSA_OK || div.units == 1) return st;
   return launch_paged_join(P, s);
 }

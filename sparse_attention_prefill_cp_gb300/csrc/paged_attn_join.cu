@@ -12,21 +12,42 @@ constexpr int kTeams = kThreads / kTeam;
 constexpr int kBatch = 4;               // parts whose loads are in flight together
 constexpr int kBlocksPerSm = 2;
 
+// Part k of the query that starts in `unit`, of head h: part 2u + 1 is of the query
+// that starts in unit u, part 2u of the one that goes on there.
+__device__ __forceinline__ int64_t part_at(const PagedAttnParams &P, int unit, int h, int k) {
+  return static_cast<int64_t>(k == 0 ? 2 * unit + 1 : 2 * (unit + k)) * P.H + h;
+}
+
+__device__ __forceinline__ void add_part(float4 &acc, const float4 &x, float w) {
+  acc.x += w * x.x;
+  acc.y += w * x.y;
+  acc.z += w * x.z;
+  acc.w += w * x.w;
+}
+
+__device__ __forceinline__ void store_head(const PagedAttnParams &P, int query, int h, int col, const float4 &acc, float l,
+                                           float m) {
+  const bool empty = l == 0.f;
+  if (P.sink && !empty) l += ex2(P.sink[h] * 1.4426950408889634f - m);
+  const float inv = empty ? 0.f : 1.f / l;
+  *reinterpret_cast<uint2 *>(P.out + (static_cast<int64_t>(query) * P.H + h) * kPagedDv + 4 * col) =
+      make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+}
+
 // A unit's join is that of the query that starts in it and ends in a later one,
-// from the query's parts in the units' order.  Part 2u + 1 is of the query that
-// starts in unit u, part 2u of the one that goes on there.  The weights are
-// e^(m_s - m) with m the largest.  As many blocks as the SMs hold go through the
-// joins, a team of a block a head at a time; where there are so few joins (one
-// long request: 74 parts a head) that the blocks would suffice for a head each, a
-// block takes a quarter of a head's columns, its warps every 16th part, and their
-// sums are added in the warps' order.  The values of the first parts are requested
-// before the maximum is known.  What bounds it: the parts, read once, and below
-// that two barriers and two dependent loads.
+// from the query's parts in the units' order.  The weights are e^(m_s - m) with m
+// the largest.  As many blocks as the SMs hold go through the joins, a team of a
+// block a head at a time; where there are so few joins (one long request: 74 parts
+// a head) that the blocks suffice for a head each, a block takes one head, its
+// warps every 16th part, and their sums are added in the warps' order.  Values are
+// requested before the maximum is known.  What bounds it: the parts, read once, and
+// below that the barriers and dependent loads of one item, 3 us (of 74 parts: by
+// teams 7).
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_join_kernel(const PagedAttnParams P) {
   __shared__ int32_t units[kThreads];
   __shared__ int32_t counts[kWarps];
-  __shared__ float4 sums[kWarps][32];
-  __shared__ float lsum[kWarps];
+  __shared__ float weight[kThreads], wsum[kWarps], wmax[kWarps];
+  __shared__ float4 sums[kWarps][kTeam];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel may still run
   // the units with a join, in order
@@ -42,74 +63,96 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_join_kernel(cons
   }
   if (has) units[at] = tid;
   __syncthreads();
-  const bool wide = n * P.H <= static_cast<int>(gridDim.x);
-  const int team = wide ? warp : tid / kTeam, step = wide ? kWarps : 1, first = wide ? warp : 0;
-  const int per = wide ? 4 : 1;  // items of a block's turn: quarters of a head, or one for each team
-  const int items = n * P.H * per;
-  for (int item = wide ? blockIdx.x : blockIdx.x * kTeams + team; item < items; item += gridDim.x * (wide ? 1 : kTeams)) {
-    const int vh = wide ? item >> 2 : item, v = vh / P.H, h = vh - v * P.H;
-    const int unit = units[v];
-    const int col = wide ? (item & 3) * 32 + lane : tid % kTeam;
+  const int items = n * P.H;
+  if (items <= static_cast<int>(gridDim.x)) {
+    const int item = blockIdx.x;
+    if (item >= items) return;
+    const int v = item / P.H, h = item - v * P.H, unit = units[v];
     const int2 join = P.joins[unit];
     const int parts = join.y - unit + 1;
-    auto part = [&](int k) { return static_cast<int64_t>(k == 0 ? 2 * unit + 1 : 2 * (unit + k)) * P.H + h; };
+    float4 x[4];
+    auto request = [&](int k) {
+      const float4 *p = reinterpret_cast<const float4 *>(P.part_o + part_at(P, unit, h, min(k, parts - 1)) * kPagedDv);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) x[c] = p[32 * c + lane];
+    };
+    request(warp);
+    const float2 ml = tid < parts ? P.part_ml[part_at(P, unit, h, tid)] : make_float2(-__builtin_huge_valf(), 0.f);
+    float m = warp_max(ml.x);
+    if (lane == 0) wmax[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) m = fmaxf(m, wmax[k]);
+    const float base = m == -__builtin_huge_valf() ? 0.f : m;
+    // a part of masked rows alone has l = 0; a NaN among its logits is a NaN in l
+    const float w = ml.y != 0.f ? ex2(ml.x - base) : 0.f;
+    weight[tid] = w;
+    float l = ml.y != 0.f ? w * ml.y : 0.f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) wsum[warp] = l;
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) l += wsum[k];
+    float4 acc[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = warp; k < parts; k += kWarps) {
+      float4 now[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) now[c] = x[c];
+      request(k + kWarps);
+      const float wk = weight[k];
+      if (wk != 0.f) {  // a masked part's values are not looked at
+#pragma unroll
+        for (int c = 0; c < 4; ++c) add_part(acc[c], now[c], wk);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) sums[warp][32 * c + lane] = acc[c];
+    __syncthreads();
+    if (tid >= kTeam) return;
+    float4 all = sums[0][tid];
+#pragma unroll
+    for (int t = 1; t < kWarps; ++t) add_part(all, sums[t][tid], 1.f);
+    store_head(P, join.x, h, tid, all, l, m);
+    return;
+  }
+  const int team = tid / kTeam, col = tid % kTeam;
+  for (int item = blockIdx.x * kTeams + team; item < items; item += gridDim.x * kTeams) {
+    const int v = item / P.H, h = item - v * P.H, unit = units[v];
+    const int2 join = P.joins[unit];
+    const int parts = join.y - unit + 1;
     float4 x[kBatch];
     float2 ml[kBatch];
     auto request = [&](int k0) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int64_t p = part(min(k0 + k * step, parts - 1));
+        const int64_t p = part_at(P, unit, h, min(k0 + k, parts - 1));
         x[k] = *(reinterpret_cast<const float4 *>(P.part_o + p * kPagedDv) + col);
         ml[k] = P.part_ml[p];
       }
     };
-    request(first);
+    request(0);
     float m = -__builtin_huge_valf();
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-      const int k = k0 + lane;
-      m = fmaxf(m, warp_max(k < parts ? P.part_ml[part(k)].x : -__builtin_huge_valf()));
-    }
+    for (int k0 = 0; k0 < parts; k0 += 32)
+      m = fmaxf(m, warp_max(k0 + lane < parts ? P.part_ml[part_at(P, unit, h, k0 + lane)].x : -__builtin_huge_valf()));
     const float base = m == -__builtin_huge_valf() ? 0.f : m;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
-    for (int k0 = first; k0 < parts; k0 += kBatch * step) {
-      if (k0 != first) request(k0);
+    for (int k0 = 0; k0 < parts; k0 += kBatch) {
+      if (k0) request(k0);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        // a part of masked rows alone has l = 0; a NaN among its logits is a NaN in l
-        if (k0 + k * step < parts && ml[k].y != 0.f) {
+        if (k0 + k < parts && ml[k].y != 0.f) {
           const float w = ex2(ml[k].x - base);
           l += w * ml[k].y;
-          acc.x += w * x[k].x;
-          acc.y += w * x[k].y;
-          acc.z += w * x[k].z;
-          acc.w += w * x[k].w;
+          add_part(acc, x[k], w);
         }
       }
     }
-    if (wide) {  // an item is the whole block's here, so all threads come by
-      sums[warp][lane] = acc;
-      if (lane == 0) lsum[warp] = l;
-      __syncthreads();
-      if (warp == 0) {
-#pragma unroll
-        for (int t = 1; t < kWarps; ++t) {
-          const float4 y = sums[t][lane];
-          acc.x += y.x;
-          acc.y += y.y;
-          acc.z += y.z;
-          acc.w += y.w;
-          l += lsum[t];
-        }
-      }
-      __syncthreads();
-      if (warp != 0) continue;
-    }
-    const bool empty = l == 0.f;
-    if (P.sink && !empty) l += ex2(P.sink[h] * 1.4426950408889634f - m);
-    const float inv = empty ? 0.f : 1.f / l;
-    const uint2 r = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2 *>(P.out + (static_cast<int64_t>(join.x) * P.H + h) * kPagedDv + 4 * col) = r;
+    store_head(P, join.x, h, col, acc, l, m);
   }
 }
 

@@ -11,9 +11,9 @@
 // is a thread's own loop.  Warps: sums, a warpgroup for each of four queries or two
 // that take the tiles of one by turns; MMA issue; four that gather the mean keys
 // by cp.async into a ring of tiles, page numbers a tile ahead.  Scores stay
-// in shared memory as order-preserving integers, from where a team of the warps of
-// a query takes its keys into registers, finds the cut bit by bit from counts (the
-// search ends as soon as a count fits) and writes the list in page order.
+// in shared memory as order-preserving integers, from where the warps of a query
+// take them into registers, find the cut from counts and write the list in page
+// order.
 //
 // What bounds it: a group of four queries and 1,024 pages takes 8 x 1,024 cycles
 // of MMA; gathering a tile and summing one take about as long, and the start and
@@ -73,14 +73,17 @@ __device__ __forceinline__ uint32_t ordered(float s) {
 // Barrier among the warps of a team.
 template <int W>
 __device__ __forceinline__ void team_sync(int team) {
-  if (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(W * 32) : "memory");
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(W * 32) : "memory");
 }
 
 // The choice of one query by a team of W warps; `team` numbers the barrier, w the
-// warp.  Warp w holds keys [w * per, w * per + per) of kq, a lane every 32nd.
+// warp.  Warp w holds keys [w * per, w * per + per) of kq, a lane every 32nd.  The
+// cut, the least key that is taken, is found from counts of the keys that reach a
+// value: bit by bit by the team (a barrier each) until at most 32 keys share the
+// bits found, then from those alone, one to a lane of every warp.
 template <int W>
 __device__ __forceinline__ void choose(const uint32_t *kq, int have, int nsel, int team, int w, int lane, int32_t *counts,
-                                       int32_t *out) {
+                                       uint32_t *near, int32_t *out) {
   constexpr int kHeld = 8;  // keys a lane keeps in registers
   if (have <= nsel) {
     for (int k = w * 32 + lane; k < nsel; k += W * 32) out[k] = k < have ? k : -1;
@@ -88,20 +91,14 @@ __device__ __forceinline__ void choose(const uint32_t *kq, int have, int nsel, i
   }
   const int per = (have + 32 * W - 1) / (32 * W) * 32, first = w * per, rounds = per / 32;
   uint32_t v[kHeld];
-  auto take = [&](int k0) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      const int b = first + (k0 + k) * 32 + lane;
-      v[k] = k0 + k < rounds && b < have ? kq[b] : 0u;  // no key is 0
-    }
-  };
-  take(0);
-  // how many keys of the team reach c; two sets of counts by turns, so that one barrier a count is enough
-  int turn = 0;
-  auto reach = [&](uint32_t c) {
-    int n = 0;
+  for (int k = 0; k < kHeld; ++k) {
+    const int b = first + k * 32 + lane;
+    v[k] = k < rounds && b < have ? kq[b] : 0u;  // no key is 0
+  }
+  auto each = [&](auto f) {  // of the lane's keys
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) n += v[k] >= c;
+    for (int k = 0; k < kHeld; ++k) f(v[k]);
     for (int k0 = kHeld; k0 < rounds; k0 += kHeld) {
       uint32_t x[kHeld];
 #pragma unroll
@@ -110,64 +107,77 @@ __device__ __forceinline__ void choose(const uint32_t *kq, int have, int nsel, i
         x[k] = k0 + k < rounds && b < have ? kq[b] : 0u;
       }
 #pragma unroll
-      for (int k = 0; k < kHeld; ++k) n += x[k] >= c;
+      for (int k = 0; k < kHeld; ++k) f(x[k]);
     }
+  };
+  // the team's sum of a count, and that of the warps before; sets of counts by turns, so that one barrier is enough
+  int turn = 0;
+  auto team_sum = [&](int n, int &before) {
     n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
-    if (W == 1) return n;
     int32_t *set = counts + turn * 16 + team * W;
     turn ^= 1;
     if (lane == 0) set[w] = n;
     team_sync<W>(team);
-    n = 0;
+    n = before = 0;
 #pragma unroll
-    for (int k = 0; k < W; ++k) n += set[k];
+    for (int k = 0; k < W; ++k) {
+      if (k < w) before += set[k];
+      n += set[k];
+    }
     return n;
   };
-  // the largest cut that at least nsel keys reach, or any that exactly nsel reach
   uint32_t cut = 0;
-  int n = have;
-  for (int bit = 31; bit >= 0 && n != nsel; --bit) {
+  int n = have, above = 0, bit = 31, skip;  // keys that reach the cut, and that reach beyond its bits
+  for (; bit >= 0 && n != nsel && n - above > 32; --bit) {
     const uint32_t c = cut | 1u << bit;
-    const int m = reach(c);
+    int m = 0;
+    each([&](uint32_t key) { m += key >= c; });
+    m = team_sum(m, skip);
     if (m >= nsel) {
       cut = c;
       n = m;
+    } else {
+      above = m;
+    }
+  }
+  if (n != nsel && bit >= 0) {
+    // the keys with the bits found, in any order: the warps write them down one after another
+    int mine = 0;
+    auto shares = [&](uint32_t key) { return key != 0u && key >= cut && (key - cut) >> bit <= 1u; };
+    each([&](uint32_t key) { mine += shares(key); });
+    int at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, at, o);
+      if (lane >= o) at += y;
+    }
+    at -= mine;
+    const int total = team_sum(mine, skip);
+    at += skip;
+    uint32_t *list = near + 32 * team;
+    each([&](uint32_t key) {
+      if (shares(key)) list[at++] = key;
+    });
+    team_sync<W>(team);
+    const uint32_t mykey = lane < total ? list[lane] : 0u;
+    for (; bit >= 0 && n != nsel; --bit) {
+      const uint32_t c = cut | 1u << bit;
+      const int m = above + __popc(__ballot_sync(0xffffffffu, mykey >= c));
+      if (m >= nsel) {
+        cut = c;
+        n = m;
+      }
     }
   }
   // keys above the cut are all taken; of those equal to it the first `ties`
-  int above = 0, equal = 0;
-  auto tally = [&](uint32_t key) {
-    above += key > cut;
+  int more = 0, equal = 0;
+  each([&](uint32_t key) {
+    more += key > cut;
     equal += key == cut;
-  };
-#pragma unroll
-  for (int k = 0; k < kHeld; ++k) tally(v[k]);
-  for (int k = kHeld; k < rounds; ++k) {
-    const int b = first + k * 32 + lane;
-    tally(b < have ? kq[b] : 0u);
-  }
-  above = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(above)));
-  equal = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(equal)));
-  int at = 0, tied = 0, ties = nsel;  // list entries and ties of the warps before; ties to take
-  if (W > 1) {
-    team_sync<W>(team);  // the last counts have been read
-    int32_t *set = counts + team * W;
-    if (lane == 0) {
-      set[w] = above;
-      set[16 + w] = equal;
-    }
-    team_sync<W>(team);
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      ties -= set[k];
-      if (k < w) {
-        at += set[k];
-        tied += set[16 + k];
-      }
-    }
-  } else {
-    ties -= above;
-  }
+  });
+  int at, tied;
+  int ties = nsel - team_sum(more, at);
+  team_sum(equal, tied);
   at += min(tied, ties);
   ties = max(ties - tied, 0);
   const uint32_t below = (1u << lane) - 1u;
@@ -350,13 +360,22 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + q * kHI;
     const float *wq = ws + q * kHI;
     const int have = misc[8 + q];
+    auto release = [&](int buf) {  // the accumulator is in registers
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&a_free[buf]);
+    };
     for (int q0 = 0; ok && q0 < QT;) {
       const Run r = run_at(q0);
+      const bool mine = q >= r.q0 && q < r.q1;
+      auto page_of = [&](int b) { return mine && b < have ? r.row[b] : 0; };  // a turn ahead
+      const int first = QT == 1 ? wg : 0, step = QT == 1 ? C::kBufs : 1;
+      int next = page_of(first * kRows + (warp & 3) * 32 + lane);
       for (int t = 0; t < r.tiles; ++t, ++tile) {
         if (QT == 1 && tile % C::kBufs != wg) continue;
         const int buf = tile % C::kBufs, b = t * kRows + (warp & 3) * 32 + lane;
-        const bool mine = q >= r.q0 && q < r.q1;
-        const int page = mine && b < have ? r.row[b] : 0;
+        const int page = next;
+        next = page_of(b + step * kRows);
         ok = __all_sync(0xffffffffu, wait_for(&a_full[buf], (tile / C::kBufs) & 1, failed, 96, tile));
         if (!ok) break;
         tc_fence_after();
@@ -367,6 +386,7 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
             uint32_t x[32];
             tmem_ld32(lane_base + buf * C::N + 32 * half, x);
             tmem_ld_wait();
+            if (half == 1) release(buf);
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
               const float4 w4 = *reinterpret_cast<const float4 *>(wq + 32 * half + k);
@@ -387,10 +407,9 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
           }
           if (b < P.keep_first || b >= have - P.keep_last) key = 0xffffffffu;
           keys[q * ld + b] = key;
+        } else {
+          release(buf);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&a_free[buf]);
       }
       q0 = r.q1;
     }
@@ -405,7 +424,7 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
     const int q = warp / C::kTeamWarps, i = i0 + q;
     if (i < P.n && P.lens[i] >= 0)
       choose<C::kTeamWarps>(keys + q * ld, misc[8 + q], P.nsel, q, warp % C::kTeamWarps, lane, misc + 16,
-                            P.out + static_cast<int64_t>(i) * P.nsel);
+                            reinterpret_cast<uint32_t *>(smem), P.out + static_cast<int64_t>(i) * P.nsel);
   }
   if (tid == 0 && *failed) record_error(P.err, DSA_ERR_DEVICE_TIMEOUT, *failed >> 24, *failed & 0xffffff);
   if (tid == 0 && bad[0]) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, bad[0], bad[1]);

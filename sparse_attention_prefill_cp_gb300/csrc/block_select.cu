@@ -40,11 +40,11 @@ struct SelectParams {
   int *err;
 };
 
-template <int QT_>
+template <int QT_, int kStages_>
 struct SelCfg {
   static constexpr int QT = QT_;  // queries of a group
   static constexpr int N = QT * kHI;
-  static constexpr int kStages = QT == 1 ? 2 : 3;   // tiles in the ring (one query: two CTAs fit an SM)
+  static constexpr int kStages = kStages_;          // tiles in the ring
   static constexpr int kBufs = 2;                   // accumulators
   static constexpr int kSumWarps = QT == 1 ? 8 : 16, kTeamWarps = kSumWarps / QT;
   static constexpr int kMmaWarp = kSumWarps, kFirstLoadWarp = kMmaWarp + 1;
@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
     // knows the page of row 8 (l / 2) + 2w + l % 2.  A tile is handed on when the next one's copies are on their way.
     const int w = warp - C::kFirstLoadWarp, u = lane & 15, my_row = 8 * (lane >> 1) + 2 * w + (lane & 1);
     const uint32_t to = smem_u32(smem) + (u >> 3) * kChunkBytes;
+    bool landed = true;  // the tile before has been handed on
     auto land = [&](int t) {
       fence_proxy_async_smem();
       __syncwarp();
@@ -310,6 +311,12 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
         const int page = next >= 0 && next < P.num_pages ? next : -1;
         next = lookup(t + 1);
         const int s = tile % C::kStages;
+        // no place for this tile yet: hand the one before on first
+        if (!landed && !__all_sync(0xffffffffu, mbar_test(&k_free[s], ((tile / C::kStages) & 1) ^ 1))) {
+          cp_async_wait<0>();
+          land(tile - 1);
+          landed = true;
+        }
         ok = __all_sync(0xffffffffu, wait_for(&k_free[s], ((tile / C::kStages) & 1) ^ 1, failed, 93, tile));
         if (!ok) break;
 #pragma unroll
@@ -319,15 +326,16 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
                       P.keys + static_cast<int64_t>(max(pg, 0)) * (kDI / 8) + u, pg >= 0 ? 16u : 0u);
         }
         cp_async_commit();
-        if (tile > 0) {
+        if (!landed) {
           cp_async_wait<1>();
           land(tile - 1);
         }
+        landed = false;
       }
       q0 = r.q1;
     }
     cp_async_wait<0>();
-    if (ok && tile > 0) land(tile - 1);
+    if (ok && !landed) land(tile - 1);
   } else if (warp == C::kMmaWarp) {
     // ---------------- MMA issue: the whole warp runs the loop, one elected lane issues
     const bool issuer = elect_one();
@@ -466,7 +474,7 @@ extern "C" dsa_status dsa_block_select(const void *q_idx, const float *w, int32_
       static_cast<int64_t>(n) * nsel > INT32_MAX)
     return DSA_ERR_SHAPE;
   if (!req && n > batch) return DSA_ERR_SHAPE;
-  if (HI < 1 || HI > kHI || DI != kDI || shift < 0 || smem_bytes<SelCfg<1>>(max_pages) > kMaxSmem)
+  if (HI < 1 || HI > kHI || DI != kDI || shift < 0 || smem_bytes<SelCfg<1, 2>>(max_pages) > kMaxSmem)
     return DSA_ERR_UNSUPPORTED;
   if (n == 0) return DSA_OK;
   if (!q_idx || !w || !block_keys || !page_table || !lens || !blocks) return DSA_ERR_INVALID_ARG;
@@ -492,7 +500,10 @@ extern "C" dsa_status dsa_block_select(const void *q_idx, const float *w, int32_
   P.keep_last = keep_last;
   P.err = err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // four queries share a request's keys where queries may share requests, once they fill the SMs
-  if (req && n >= 2 * num_sms() && smem_bytes<SelCfg<4>>(max_pages) <= kMaxSmem) return launch<SelCfg<4>>(P, s);
-  return launch<SelCfg<1>>(P, s);
+  // four queries share a request's keys where queries may share requests, once they fill the SMs (400 queries of 625
+  // blocks: 14 against 17 us); one query a CTA has two of them on an SM, or, where there are no more queries than SMs, a
+  // longer ring (64 of 1,024 blocks: 11 against 12 us)
+  if (req && n >= 2 * num_sms() && smem_bytes<SelCfg<4, 3>>(max_pages) <= kMaxSmem) return launch<SelCfg<4, 3>>(P, s);
+  if (n <= num_sms() && smem_bytes<SelCfg<1, 4>>(max_pages) <= kMaxSmem) return launch<SelCfg<1, 4>>(P, s);
+  return launch<SelCfg<1, 2>>(P, s);
 }

@@ -448,8 +448,8 @@ constexpr size_t kMaxSmem = 227 * 1024;
 template <class C>
 dsa_status launch(const SelectParams &P, cudaStream_t stream) {
   const size_t bytes = smem_bytes<C>(P.max_pages);
-  cudaError_t e = cudaFuncSetAttribute(block_select_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(kMaxSmem));
+  static std::atomic<uint64_t> devices{0};
+  cudaError_t e = allow_smem(block_select_kernel<C>, static_cast<int>(kMaxSmem), devices);
   if (e != cudaSuccess) return cuda_fail(e);
   e = launch_overlapped(block_select_kernel<C>, dim3(static_cast<unsigned>((P.n + C::QT - 1) / C::QT)), C::kThreads, bytes,
                         stream, P);

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/dsa_cp.h"
 
 namespace dsa {
@@ -21,6 +23,20 @@ dsa_status cuda_fail_msg(const char *msg);
 inline dsa_status check_launch() {
   cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? DSA_OK : cuda_fail(e);
+}
+
+// Shared memory beyond 48 KB for a kernel, asked for once per device (a call of it
+// costs the host half a microsecond).
+template <typename... Params>
+cudaError_t allow_smem(void (*kernel)(Params...), int bytes, std::atomic<uint64_t> &devices) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (devices.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) devices.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // Launch of a kernel that may become resident while the kernel before it in the

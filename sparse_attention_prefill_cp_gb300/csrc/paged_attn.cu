@@ -682,7 +682,8 @@ dsa_status launch(const CUtensorMap &kv_map, const void *q, const PagedAttnParam
   dsa_status st = encode_tensor_map(&q_map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q, dims, strides, box,
                                     CU_TENSOR_MAP_SWIZZLE_128B);
   if (st != DSA_OK) return st;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<uint64_t> devices{0};
+  cudaError_t e = allow_smem(paged_attn_kernel<C>, C::kSmemBytes, devices);
   if (e != cudaSuccess) return cuda_fail(e);
   e = launch_overlapped(paged_attn_kernel<C>, dim3(static_cast<unsigned>(P.units * P.groups)), C::kThreads, C::kSmemBytes,
                         stream, q_map, kv_map, P);

@@ -61,6 +61,13 @@ struct SelCfg {
   static constexpr uint32_t kIdesc = idesc_bf16(kRows, N, false, false);
 };
 
+// ReLU that keeps a NaN (fmaxf makes it 0).
+__device__ __forceinline__ float relu(uint32_t x) {
+  float y;
+  asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(y) : "f"(__uint_as_float(x)));
+  return y;
+}
+
 // Scores to integers of the same order; a NaN is below every number, 0 is kept
 // for pages that do not take part.
 __device__ __forceinline__ uint32_t ordered(float s) {
@@ -398,10 +405,8 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
 #pragma unroll
             for (int k = 0; k < 32; k += 4) {
               const float4 w4 = *reinterpret_cast<const float4 *>(wq + 32 * half + k);
-              s[0] = f2_fma(f2_pack(w4.x, w4.y),
-                            f2_pack(fmaxf(__uint_as_float(x[k]), 0.f), fmaxf(__uint_as_float(x[k + 1]), 0.f)), s[0]);
-              s[1] = f2_fma(f2_pack(w4.z, w4.w),
-                            f2_pack(fmaxf(__uint_as_float(x[k + 2]), 0.f), fmaxf(__uint_as_float(x[k + 3]), 0.f)), s[1]);
+              s[0] = f2_fma(f2_pack(w4.x, w4.y), f2_pack(relu(x[k]), relu(x[k + 1])), s[0]);
+              s[1] = f2_fma(f2_pack(w4.z, w4.w), f2_pack(relu(x[k + 2]), relu(x[k + 3])), s[1]);
             }
           }
           float s0, s1, s2, s3;

@@ -664,7 +664,7 @@ PagedDivision divide(int64_t n, int H, int max_pages, int nsel, int shift) {
   d.group_heads = H <= 16 ? 16 : H <= 32 ? 32 : 64;
   d.groups = (H + d.group_heads - 1) / d.group_heads;
   const int64_t blocks = n * paged_blocks(INT32_MAX, nsel, max_pages, shift);
-  const int64_t fit = num_sms() / d.groups > 0 ? num_sms() / d.groups : 1;
+  const int64_t fit = num_sms() / d.groups > 0 ? num_sms() / d.groups : 1;  // below the join's 512
   d.units = static_cast<int>(blocks < fit ? blocks : fit);
   return d;
 }

@@ -215,6 +215,21 @@ def test_values_that_are_not_finite():
     near(dsa.dsa_paged_attn(q.cuda(), cache, table, i32(short), SCALE, DV), *attend64(q, rows, short))
 
 
+@pytest.mark.parametrize("bad", [NAN, INF, -INF])
+def test_a_query_that_is_not_finite_spoils_its_head_alone(bad):
+    lens, P, H = [1000, 300], 64, 40
+    cache, table, rows = paged(lens, P, seed=29)
+    q = randn(2, H, D, seed=30)
+    clean = q.clone()
+    q[0, 33, 7] = bad
+    q[1, 2, 575] = bad
+    got = dsa.dsa_paged_attn(q.cuda(), cache, table, i32(lens), SCALE, DV)
+    assert torch.isnan(got[0, 33]).all() and torch.isnan(got[1, 2]).all()
+    want, tol = attend64(clean, rows, lens)
+    want[0, 33] = want[1, 2] = NAN
+    near(got, want, tol)
+
+
 def test_sinks_of_every_size():
     lens, P, H = [200, 0, 1], 32, 4
     cache, table, rows = paged(lens, P, seed=11)
@@ -575,6 +590,7 @@ def test_scores_that_are_no_numbers_and_pages_that_are_none():
     q, w = grid(2, 64, 128, std=1, step=0.25, seed=2), grid(2, 64, std=0.125, step=1 / 32, seed=3).abs()
     keys = grid(width, 128, std=0.5, step=1 / 32, seed=4)
     w[0, 3] = NAN                                   # every score of that query
+    keys[11, 5] = NAN                               # the scores of that page
     table[1, 7] = -1                                # ranks last
     table[1, 9] = width
     lens = [width * P] * 2
@@ -582,7 +598,7 @@ def test_scores_that_are_no_numbers_and_pages_that_are_none():
                                i32(lens), P, nsel)
     assert bounds(57) == 1
     assert got[0].tolist() == [0, 1, 2, 29]
-    keep = [b for b in range(width) if b not in (7, 9)]
+    keep = [b for b in range(width) if b not in (7, 9, 11)]
     want = O.block_select(q[1].numpy(), w[1].numpy(), keys.numpy(), keep, len(keep) * P, P, nsel)
     assert got[1].tolist() == [keep[b] for b in want]
     dsa.dsa_block_select(q.to(torch.bfloat16).cuda(), w.cuda(), keys.to(torch.bfloat16).cuda(), table[:1].cuda(),
@@ -673,3 +689,60 @@ def test_serving_steps(H, P):
     assert count.item() == pool - owned
     dsa.dsa_pages_update(table, i32(lens), i32([0] * B), free, count, P)
     assert count.item() == pool and sorted(free.tolist()) == list(range(pool)) and (table == -1).all()
+
+
+@pytest.mark.parametrize("H", [16, 128])
+def test_steps_in_a_graph(H):
+    """A whole step captured once and replayed: lengths grow, pages are taken, rows written, blocks chosen and attended
+    over, all by what lies in the step's own tensors; every replay against the calls one by one."""
+    P, B, width, pool, nsel, steps = 16, 3, 8, 20, 3, 40
+    start = [15, 0, 47]
+
+    def fresh():
+        s = dict(table=torch.full((B, width), -1, dtype=torch.int32, device="cuda"), free=i32(list(range(pool))),
+                 count=i32([pool]), held=i32([0] * B), seq=i32(start),
+                 cache=torch.full((pool, P, D), NAN, dtype=torch.bfloat16, device="cuda"),
+                 keys=torch.zeros(pool, P, 128, dtype=torch.bfloat16, device="cuda"),
+                 means=torch.zeros(pool, 128, dtype=torch.bfloat16, device="cuda"),
+                 kv=torch.zeros(B, D, dtype=torch.bfloat16, device="cuda"),
+                 ki=torch.zeros(B, 128, dtype=torch.bfloat16, device="cuda"),
+                 q=torch.zeros(B, H, D, dtype=torch.bfloat16, device="cuda"),
+                 qi=torch.zeros(B, 64, 128, dtype=torch.bfloat16, device="cuda"),
+                 w=torch.ones(B, 64, device="cuda"))
+        n = sum(start)
+        dsa.dsa_pages_update(s["table"], s["held"], s["seq"], s["free"], s["count"], P)
+        slots = dsa.dsa_pages_slots(s["table"], s["held"], s["seq"], P, n)
+        dsa.dsa_pages_append(randn(n, D, seed=1).cuda(), randn(n, 128, seed=2).cuda(), slots, s["cache"], s["keys"],
+                             s["means"])
+        s["held"].copy_(s["seq"])
+        return s
+
+    def step(s):
+        s["seq"].add_(1)
+        dsa.dsa_pages_update(s["table"], s["held"], s["seq"], s["free"], s["count"], P)
+        slots = dsa.dsa_pages_slots(s["table"], s["held"], s["seq"], P, B)
+        dsa.dsa_pages_append(s["kv"], s["ki"], slots, s["cache"], s["keys"], s["means"])
+        blocks = dsa.dsa_block_select(s["qi"], s["w"], s["means"], s["table"], s["seq"], P, nsel)
+        out = dsa.dsa_paged_attn(s["q"], s["cache"], s["table"], s["seq"], SCALE, DV, blocks=blocks)
+        s["held"].copy_(s["seq"])
+        return blocks, out
+
+    def inputs(s, t):
+        for k, name in enumerate(("kv", "ki", "q", "qi")):
+            s[name].copy_(randn(*s[name].shape, seed=100 * t + k))
+
+    a, b = fresh(), fresh()
+    step(fresh())                                    # warm
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(a)
+    for t in range(steps):
+        inputs(a, t)
+        inputs(b, t)
+        graph.replay()
+        want = step(b)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), t
+    for name in ("table", "free", "count", "keys", "means"):
+        assert torch.equal(a[name], b[name])
+    assert a["seq"].tolist() == [n + steps for n in start] and not torch.isnan(got[1]).any()

@@ -33,6 +33,7 @@
  *     kept addresses are stale, so do not use the library on that device
  *     again in the same process.
  *   - Supported dimension sets (others return DSA_ERR_UNSUPPORTED):
+ *       (the calls over caches say theirs)
  *       DeepSeek-V3.2 shapes: H=128, D=576, Dv=512, HI=64, DI=128, topk=2048
  *       tiny shapes:          H=8,   D=64,  Dv=48,  HI=4,  DI=32,  topk=64
  */

@@ -34,6 +34,13 @@
 // MMA (each weight within 2^-8 of itself); logits, sums and O are fp32.  Rows
 // behind a query's last position hold anything, NaN included: they are zeroed in
 // shared memory, since 0 * NaN would reach O.
+//
+// What bounds it: with up to 32 heads HBM (64 requests of 8,192 rows, 16 heads: 106
+// us with the join, 5.7 TB/s; 64 heads 119 us).  With 128 heads shared memory: a
+// block of 64 heads moves 578 KB (operands of QK and PV 415, TMA 147, P 16), 4,520
+// cycles, and takes 5,850, since Q and one block fill the 227 KB and nothing of the
+// next lands while the softmax runs: 64 requests of 8,192 rows 189 us, 2,048 queries
+// of 2,048 rows 1,384 us, 844 TFLOP/s.
 #include "internal.h"
 #include "paged_attn.cuh"
 

@@ -62,7 +62,7 @@ __device__ __forceinline__ uint2 scan_pair(uint2 x, uint2 &total, uint2 *warp_su
 // result depends on nothing but the inputs.  1,024 requests at a time: a scan
 // numbers their pages, then the threads share the pages out evenly, each finding
 // its page's request by bisection (a warp a request instead: 20 against 5 us for
-// 16 prompts of 184,265 rows).  Everything is checked before anything is written.
+// 16 prompts of 68,569 rows).  Everything is checked before anything is written.
 // One block: a step of a decode batch touches a page in P requests, and is a
 // launch and four dependent loads long.
 __global__ void __launch_bounds__(kUpdateThreads) pages_update_kernel(const PagesUpdate P) {
@@ -210,7 +210,8 @@ constexpr int kMaxKeyUnits = 16;  // half a warp
 // makes the page's mean key.  The keys of the page's rows come from this call's
 // input as far as its tokens are the page's rows, else from the key cache; half
 // warp h sums rows h, h + 2, .. in fp32, and the halves are added, so a page's
-// key has the same bits however its rows arrived.
+// key has the same bits however its rows arrived.  61 rows 3.5 us (a launch and
+// three dependent loads), 8,000 rows 5.8 us, 3.9 TB/s (a launch and its ramp).
 __global__ void __launch_bounds__(kAppendWarps * 32) pages_append_kernel(const PagesAppend A) {
   const int t = static_cast<int>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (t >= A.n) return;

@@ -9,13 +9,12 @@ PyTorch only provides device memory and streams.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import functools
 
 import torch
 
-from ._lib import DSAError, LocalMetadata, check, load  # noqa: F401
+from ._lib import DSAError, LocalMetadata, binding, check, load  # noqa: F401
 
 IN_SEQ_SPLIT = 0
 ROUND_ROBIN = 1
@@ -628,9 +627,6 @@ def _launch_on(stream, ref: torch.Tensor, *others):
     return (None if here and stream.cuda_stream == handle else torch.cuda.stream(stream)), stream.cuda_stream
 
 
-_HERE = contextlib.nullcontext()
-
-
 def _int32(**sizes: int) -> None:
     """Refuse sizes that the C ABI's int32 arguments would take modulo 2^32."""
     for name, v in sizes.items():
@@ -810,58 +806,14 @@ def dsa_sparse_attn_int4kv(q: torch.Tensor, kv_cache: torch.Tensor, topk_idx: to
     return out
 
 
-PAGE_SIZES = (16, 32, 64, 128)
+# The calls over the paged latent cache are those of a decode step: their checks,
+# outputs and workspaces are in the native binding (csrc/binding.cpp).
 
-
-def _page_size(P: int) -> int:
-    if P not in PAGE_SIZES:
-        raise ValueError(f"pages of {P} rows: a page has one of {PAGE_SIZES}")
-    return int(P)
-
-
-_INT32_MAX = 0x7fffffff
-
-
-def _shape(t: torch.Tensor, dtype: torch.dtype, dims: int, name: str, form: str) -> torch.Size:
-    """The shape of a contiguous CUDA tensor of that type and number of dimensions."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        _need(t, dtype, name)
-    s = t.shape
-    if len(s) != dims:
-        raise ValueError(f"{name} must be {form}")
-    return s
-
-
-def _need_table(page_table: torch.Tensor) -> torch.Size:
-    s = _shape(page_table, torch.int32, 2, "page_table", "[batch, max_pages]")
-    if s[1] < 1 or s[0] * s[1] > _INT32_MAX:
-        raise ValueError("page_table must be [batch, max_pages] with a page at least and fewer than 2^31 entries")
-    return s
-
-
-def _need_ints(t: torch.Tensor, n: int, name: str) -> None:
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
-        _need(t, torch.int32, name)
-    if t.shape != (n,):
-        raise ValueError(f"{name} must be [{n}]")
-
-
-def _pages(t: torch.Tensor, name: str) -> tuple[int, int, int, int, int]:
-    """(pages, rows, columns, page stride, row stride) of a bf16 [pages, P, D]
-    tensor whose rows are contiguous and start on 16-byte boundaries."""
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or not t.is_cuda or len(t.shape) != 3:
-        raise ValueError(f"{name} must be a CUDA bfloat16 tensor [num_pages, page_size, D]")
-    R, P, D = t.shape
-    if P not in PAGE_SIZES:
-        _page_size(P)
-    if R * P > _INT32_MAX:
-        raise ValueError(f"{name} has {R * P} rows, not below 2^31")
-    page, row, one = t.stride()
-    if R < 2:
-        page = row * P
-    if one != 1 or row < D or row % 8 or page % 8 or page < (P - 1) * row + D or t.data_ptr() % 16:
-        raise ValueError(f"the rows of {name} must be contiguous, not overlap and start on 16-byte boundaries")
-    return R, P, D, page, row
+def _result(r, where: str):
+    """The result of a native call, or the error of the dsa_status that it returned."""
+    if r.__class__ is int:
+        check(r, where)
+    return r
 
 
 def dsa_pages_update(page_table: torch.Tensor, held_lens: torch.Tensor, seq_lens: torch.Tensor,
@@ -873,19 +825,8 @@ def dsa_pages_update(page_table: torch.Tensor, held_lens: torch.Tensor, seq_lens
     [1] of them free).  Where a length is out of range or the free pages do
     not suffice nothing changes, and dsa_poll_device_error tells; a call with
     the lengths exchanged undoes one."""
-    B, width = _need_table(page_table)
-    P = _page_size(page_size)
-    _need_ints(held_lens, B, "held_lens")
-    _need_ints(seq_lens, B, "seq_lens")
-    pool, = _shape(free_pages, torch.int32, 1, "free_pages", "[num_pages]")
-    if pool > _INT32_MAX:
-        raise ValueError(f"{pool} pages, not below 2^31")
-    _need_ints(free_count, 1, "free_count")
-    ctx, st = _launch_on(stream, page_table, held_lens, seq_lens, free_pages, free_count)
-    with ctx or _HERE:
-        check(load().dsa_pages_update(page_table.data_ptr(), B, width, held_lens.data_ptr(), seq_lens.data_ptr(), P,
-                                      free_pages.data_ptr(), pool, free_count.data_ptr(), st), "dsa_pages_update")
-    return page_table
+    return _result(binding().pages_update(page_table, held_lens, seq_lens, free_pages, free_count, page_size, stream),
+                   "dsa_pages_update")
 
 
 def dsa_pages_slots(page_table: torch.Tensor, first: torch.Tensor | None, seq_lens: torch.Tensor, page_size: int,
@@ -893,22 +834,8 @@ def dsa_pages_slots(page_table: torch.Tensor, first: torch.Tensor | None, seq_le
     """Slots int32 [num_slots] of the positions ``first``[b] .. ``seq_lens``[b]
     - 1 of every request (``first`` None: from 0, every KV row of the batch),
     requests in order, -1 behind the last."""
-    B, width = _need_table(page_table)
-    P = _page_size(page_size)
-    if first is not None:
-        _need_ints(first, B, "first")
-    _need_ints(seq_lens, B, "seq_lens")
-    if not 0 <= num_slots <= _INT32_MAX:
-        raise ValueError(f"num_slots = {num_slots}")
-    if out is not None:
-        _need_ints(out, num_slots, "out")
-    ctx, st = _launch_on(stream, page_table, first, seq_lens, out)
-    with ctx or _HERE:
-        if out is None:
-            out = torch.empty(num_slots, dtype=torch.int32, device=page_table.device)
-        check(load().dsa_pages_slots(page_table.data_ptr(), B, width, _addr(first), seq_lens.data_ptr(), P,
-                                     out.data_ptr(), num_slots, st), "dsa_pages_slots")
-    return out
+    return _result(binding().pages_slots(page_table, first, seq_lens, page_size, num_slots, out, stream),
+                   "dsa_pages_slots")
 
 
 def dsa_pages_append(kv: torch.Tensor, k_idx: torch.Tensor | None, slots: torch.Tensor, cache: torch.Tensor,
@@ -920,32 +847,7 @@ def dsa_pages_append(kv: torch.Tensor, k_idx: torch.Tensor | None, slots: torch.
     the mean key of every page whose last row is written into ``block_keys``
     [num_pages, DI].  Slots of one page stand together, ascending.  The rows
     of kv and of cache may lie apart, each starting on a 16-byte boundary."""
-    R, P, D, page, row = _pages(cache, "cache")
-    if not isinstance(kv, torch.Tensor) or kv.dtype != torch.bfloat16 or not kv.is_cuda or len(kv.shape) != 2 or \
-            kv.shape[1] != D:
-        raise ValueError(f"kv must be a CUDA bfloat16 tensor [n, {D}]")
-    n = kv.shape[0]
-    stride, one = kv.stride()
-    if n < 2:
-        stride = D
-    if one != 1 or stride < D or stride % 8 or kv.data_ptr() % 16:
-        raise ValueError("the rows of kv must be contiguous, not overlap and start on 16-byte boundaries")
-    if D < 8 or D % 8 or n > _INT32_MAX:
-        raise ValueError("D must be a multiple of 8, and n below 2^31")
-    _need_ints(slots, n, "slots")
-    DI = 8
-    if (k_idx is None) != (key_cache is None) or (k_idx is None) != (block_keys is None):
-        raise ValueError("k_idx, key_cache and block_keys come together")
-    if k_idx is not None:
-        for t, name in ((k_idx, "k_idx"), (key_cache, "key_cache"), (block_keys, "block_keys")):
-            _need(t, torch.bfloat16, name)
-        DI = k_idx.shape[-1]
-        if tuple(k_idx.shape) != (n, DI) or tuple(key_cache.shape) != (R, P, DI) or tuple(block_keys.shape) != (R, DI):
-            raise ValueError(f"k_idx must be [{n}, DI], key_cache [{R}, {P}, DI] and block_keys [{R}, DI]")
-    ctx, st = _launch_on(stream, cache, kv, k_idx, slots, key_cache, block_keys)
-    with ctx or _HERE:
-        check(load().dsa_pages_append(kv.data_ptr(), stride, _addr(k_idx), slots.data_ptr(), n, D, DI, cache.data_ptr(),
-                                      page, row, R, P, _addr(key_cache), _addr(block_keys), st), "dsa_pages_append")
+    _result(binding().pages_append(kv, k_idx, slots, cache, key_cache, block_keys, stream), "dsa_pages_append")
 
 
 def dsa_block_select(q_idx: torch.Tensor, w: torch.Tensor, block_keys: torch.Tensor, page_table: torch.Tensor,
@@ -958,31 +860,8 @@ def dsa_block_select(q_idx: torch.Tensor, w: torch.Tensor, block_keys: torch.Ten
     ``keep_first`` and last ``keep_last`` of its pages are always among them,
     the others by the indexer score of their mean keys.  A query with a
     negative length has no row: ``out`` keeps what is there."""
-    n, HI, DI = _shape(q_idx, torch.bfloat16, 3, "q_idx", "[n, HI, DI]")
-    if _shape(w, torch.float32, 2, "w", "[n, HI]") != (n, HI):
-        raise ValueError(f"w must be [{n}, {HI}]")
-    R, DK = _shape(block_keys, torch.bfloat16, 2, "block_keys", "[num_pages, DI]")
-    if DK != DI:
-        raise ValueError(f"block_keys must be [num_pages, {DI}]")
-    B, width = _need_table(page_table)
-    P = _page_size(page_size)
-    _need_ints(lens, n, "lens")
-    if req is not None:
-        _need_ints(req, n, "req")
-    elif n > B:
-        raise ValueError("more queries than requests (pass req)")
-    if R * P > _INT32_MAX or n * max(nsel, 1) > _INT32_MAX or max(HI, nsel, abs(keep_first), abs(keep_last)) > _INT32_MAX:
-        raise ValueError("sizes that are not below 2^31")
-    if out is not None and _shape(out, torch.int32, 2, "out", "[n, nsel]") != (n, nsel):
-        raise ValueError(f"out must be [{n}, {nsel}]")
-    ctx, st = _launch_on(stream, q_idx, w, block_keys, page_table, lens, req, out)
-    with ctx or _HERE:
-        if out is None:
-            out = torch.empty((n, max(nsel, 0)), dtype=torch.int32, device=q_idx.device)
-        check(load().dsa_block_select(q_idx.data_ptr(), w.data_ptr(), n, HI, DI, block_keys.data_ptr(),
-                                      R, P, page_table.data_ptr(), B, width, lens.data_ptr(),
-                                      _addr(req), nsel, keep_first, keep_last, out.data_ptr(), st), "dsa_block_select")
-    return out
+    return _result(binding().block_select(q_idx, w, block_keys, page_table, lens, page_size, nsel, keep_first, keep_last,
+                                          req, out, stream), "dsa_block_select")
 
 
 def dsa_paged_attn_workspace_size(n: int, H: int, max_pages: int, nsel: int, page_size: int) -> int:
@@ -992,11 +871,6 @@ def dsa_paged_attn_workspace_size(n: int, H: int, max_pages: int, nsel: int, pag
     check(load().dsa_paged_attn_workspace_size(n, H, max_pages, nsel, page_size, C.byref(b)),
           "dsa_paged_attn_workspace_size")
     return b.value
-
-
-@functools.lru_cache(maxsize=4096)
-def _paged_workspace(device: int, n: int, H: int, max_pages: int, nsel: int, page_size: int) -> int:
-    return dsa_paged_attn_workspace_size(n, H, max_pages, nsel, page_size)  # with that device current
 
 
 def dsa_paged_attn(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, lens: torch.Tensor,
@@ -1013,43 +887,8 @@ def dsa_paged_attn(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tenso
     leaves the query's rows of ``out`` as they are.  ``workspace``: uint8, at
     least dsa_paged_attn_workspace_size bytes, allocated per call when
     omitted."""
-    n, H, D = _shape(q, torch.bfloat16, 3, "q", "[n, H, D]")
-    R, P, Dc, page, row = _pages(cache, "cache")
-    if Dc != D:
-        raise ValueError("q / cache do not match in D")
-    B, width = _need_table(page_table)
-    _need_ints(lens, n, "lens")
-    if req is not None:
-        _need_ints(req, n, "req")
-    elif n > B:
-        raise ValueError("more queries than requests (pass req)")
-    nsel = 0
-    if blocks is not None:
-        rows, nsel = _shape(blocks, torch.int32, 2, "blocks", "[n, nsel]")
-        if rows != n or nsel < 1:
-            raise ValueError(f"blocks must be [{n}, nsel]")
-    if attn_sink is not None and _shape(attn_sink, torch.float32, 1, "attn_sink", "[H]") != (H,):
-        raise ValueError(f"attn_sink must be [{H}]")
-    if out is not None and _shape(out, torch.bfloat16, 3, "out", "[n, H, Dv]") != (n, H, Dv):
-        raise ValueError(f"out must be [{n}, {H}, {Dv}]")
-    if workspace is not None:
-        _need(workspace, torch.uint8, "workspace")
-    if n > _INT32_MAX or H > _INT32_MAX or n * nsel > _INT32_MAX:
-        raise ValueError("sizes that are not below 2^31")
-    ctx, st = _launch_on(stream, q, cache, page_table, lens, blocks, req, attn_sink, out, workspace)
-    with ctx or _HERE:
-        if out is None:
-            out = torch.empty((n, H, Dv), dtype=torch.bfloat16, device=q.device)
-        if workspace is None:
-            ws_bytes = _paged_workspace(q.get_device(), n, H, width, nsel, P)
-            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
-        else:
-            ws_bytes = workspace.numel()
-        check(load().dsa_paged_attn(q.data_ptr(), n, cache.data_ptr(), page, row, R, P, page_table.data_ptr(), B, width,
-                                    lens.data_ptr(), _addr(req), _addr(blocks), nsel, _addr(attn_sink),
-                                    float(softmax_scale), H, D, Dv, out.data_ptr(), workspace.data_ptr(), ws_bytes, st),
-              "dsa_paged_attn")
-    return out
+    return _result(binding().paged_attn(q, cache, page_table, lens, softmax_scale, Dv, blocks, req, attn_sink, out,
+                                        workspace, stream), "dsa_paged_attn")
 
 
 def dsa_poll_device_error(stream=None) -> None:

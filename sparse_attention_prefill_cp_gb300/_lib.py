@@ -5,7 +5,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 
-from .build import LIB_PATH
+from .build import BINDING_PATH, LIB_PATH
 
 c_stream = C.c_void_p
 c_i32p = C.POINTER(C.c_int32)
@@ -150,6 +150,26 @@ def load(path: str | None = None) -> C.CDLL:
     if path is None:
         _LIB = lib
     return lib
+
+
+_BINDING = None
+
+
+def binding():
+    """The native binding of the calls of a decode step (csrc/binding.cpp);
+    built first if it is missing.  Raises if it cannot be built or loaded."""
+    global _BINDING
+    if _BINDING is None:
+        load()
+        if not os.path.exists(BINDING_PATH):
+            from .build import build
+            build()
+        import importlib.util
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _BINDING = module
+    return _BINDING
 
 
 class DSAError(RuntimeError):

@@ -119,29 +119,41 @@ __device__ __forceinline__ void choose(const uint32_t *kq, int have, int nsel, i
       for (int k = 0; k < kHeld; ++k) f(x[k]);
     }
   };
-  // the team's sum of a count, and that of the warps before; sets of counts by turns, so that one barrier is enough
+  // the team's counts, a warp each, into c; sets of counts by turns, so that one barrier is enough
   int turn = 0;
-  auto team_sum = [&](int n, int &before) {
+  auto team_counts = [&](int n, int4 (&c)[W / 4]) {
     n = static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(n)));
     int32_t *set = counts + turn * 16 + team * W;
     turn ^= 1;
     if (lane == 0) set[w] = n;
     team_sync<W>(team);
-    n = before = 0;
 #pragma unroll
-    for (int k = 0; k < W; ++k) {
-      if (k < w) before += set[k];
-      n += set[k];
-    }
+    for (int k = 0; k < W / 4; ++k) c[k] = *reinterpret_cast<const int4 *>(set + 4 * k);
+  };
+  auto total_of = [&](const int4 (&c)[W / 4]) {
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < W / 4; ++k) n += (c[k].x + c[k].y) + (c[k].z + c[k].w);
     return n;
   };
+  auto before_of = [&](const int4 (&c)[W / 4]) {  // of the warps before this one
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < W / 4; ++k)
+      n += (4 * k < w ? c[k].x : 0) + (4 * k + 1 < w ? c[k].y : 0) + (4 * k + 2 < w ? c[k].z : 0);
+#pragma unroll
+    for (int k = 0; k < W / 4; ++k) n += 4 * k + 3 < w ? c[k].w : 0;
+    return n;
+  };
+  int4 c4[W / 4];
   uint32_t cut = 0;
-  int n = have, above = 0, bit = 31, skip;  // keys that reach the cut, and that reach beyond its bits
+  int n = have, above = 0, bit = 31;  // keys that reach the cut, and that reach beyond its bits
   for (; bit >= 0 && n != nsel && n - above > 32; --bit) {
     const uint32_t c = cut | 1u << bit;
     int m = 0;
     each([&](uint32_t key) { m += key >= c; });
-    m = team_sum(m, skip);
+    team_counts(m, c4);
+    m = total_of(c4);
     if (m >= nsel) {
       cut = c;
       n = m;
@@ -161,8 +173,9 @@ __device__ __forceinline__ void choose(const uint32_t *kq, int have, int nsel, i
       if (lane >= o) at += y;
     }
     at -= mine;
-    const int total = team_sum(mine, skip);
-    at += skip;
+    team_counts(mine, c4);
+    const int total = total_of(c4);
+    at += before_of(c4);
     uint32_t *list = near + 32 * team;
     each([&](uint32_t key) {
       if (shares(key)) list[at++] = key;
@@ -184,9 +197,10 @@ __device__ __forceinline__ void choose(const uint32_t *kq, int have, int nsel, i
     more += key > cut;
     equal += key == cut;
   });
-  int at, tied;
-  int ties = nsel - team_sum(more, at);
-  team_sum(equal, tied);
+  team_counts(more, c4);
+  int at = before_of(c4), ties = nsel - total_of(c4);
+  team_counts(equal, c4);
+  const int tied = before_of(c4);
   at += min(tied, ties);
   ties = max(ties - tied, 0);
   const uint32_t below = (1u << lane) - 1u;

@@ -112,6 +112,55 @@ __global__ void __launch_bounds__(kUpdateThreads) pages_update_kernel(const Page
     return total.x;
   };
   int64_t R = 0, G = 0;
+  auto refused = [&]() {
+    if (!bad[0] && count >= 0 && count + R <= P.num_pages && G <= count + R) return false;
+    if (tid == 0) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, bad[0] ? bad[0] : 54, bad[0] ? bad[1] : static_cast<int>(G));
+    return true;
+  };
+  if (P.batch <= kUpdateThreads) {
+    // one look at the lengths and one scan for both kinds (2.9 -> 2.4 us for a step of 64 requests)
+    int had, need;
+    change(tid, had, need);
+    uint2 total;
+    const uint2 before = scan_pair(make_uint2(max(had - need, 0), max(need - had, 0)), total, warp_sums);
+    R = total.x;
+    G = total.y;
+    page0[tid] = min(had, need);
+    for (int released = 1; released >= 0; --released) {
+      const uint32_t n = released ? total.x : total.y;
+      if (n == 0) {
+        if (released && refused()) return;
+        continue;
+      }
+      start[tid] = released ? before.x : before.y;
+      __syncthreads();
+      for (int write = released ? 0 : 1; write < 2; ++write) {  // releases are looked over first
+        for (uint32_t i = tid; i < n; i += kUpdateThreads) {
+          int lo = 0;
+#pragma unroll
+          for (int d = kUpdateThreads / 2; d; d >>= 1)
+            if (start[lo + d] <= i) lo += d;
+          int32_t *entry = P.table + static_cast<int64_t>(lo) * P.max_pages + page0[lo] + static_cast<int>(i - start[lo]);
+          int32_t *place = P.free_pages + (count + R - 1 - i);
+          if (!write) {
+            if (*entry < 0 || *entry >= P.num_pages) {
+              bad[0] = 53;
+              bad[1] = lo;
+            }
+          } else if (released) {
+            *place = *entry;
+            *entry = -1;
+          } else {
+            *entry = *place;
+          }
+        }
+        __syncthreads();
+        if (!write && refused()) return;
+      }
+    }
+    if (tid == 0) *P.free_count = static_cast<int32_t>(count + R - G);
+    return;
+  }
   for (int b0 = 0; b0 < P.batch; b0 += kUpdateThreads) {
     uint32_t grown;
     R += each_page(b0, true, grown, [&](int b, int k, uint32_t) {
@@ -123,10 +172,7 @@ __global__ void __launch_bounds__(kUpdateThreads) pages_update_kernel(const Page
     });
     G += grown;
   }
-  if (bad[0] || count < 0 || count + R > P.num_pages || G > count + R) {
-    if (tid == 0) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, bad[0] ? bad[0] : 54, bad[0] ? bad[1] : static_cast<int>(G));
-    return;
-  }
+  if (refused()) return;
   // releases, then growth, which may take what was released
   for (int released = 1; released >= 0; --released) {
     if ((released ? R : G) == 0) continue;

@@ -34,96 +34,117 @@ __device__ __forceinline__ void store_head(const PagedAttnParams &P, int query, 
       make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
 }
 
+// What a block's warps share.
+struct JoinShared {
+  int4 list[kThreads];    // the units with a join, in order: unit, query, last unit
+  int32_t counts[kWarps];
+  float weight[kThreads], wsum[kWarps], wmax[kWarps];
+  float4 sums[kWarps][kTeam];
+};
+
+// One head by a whole block, or NC of the four quarters of its columns from quarter
+// c0 on: warp w takes parts w, w + 16, ..; their sums are added in the warps' order.
+template <int NC>
+__device__ __forceinline__ void join_wide(const PagedAttnParams &P, JoinShared &s, int4 join, int h, int c0) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, unit = join.x, parts = join.z - unit + 1;
+  float4 x[2][NC];  // of the next two parts
+  auto request = [&](float4 (&y)[NC], int k) {
+    const float4 *p = reinterpret_cast<const float4 *>(P.part_o + part_at(P, unit, h, min(k, parts - 1)) * kPagedDv);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) y[c] = p[32 * (c0 + c) + lane];
+  };
+  request(x[0], warp);
+  if (NC < 4) request(x[1], warp + kWarps);
+  const float2 ml = tid < parts ? P.part_ml[part_at(P, unit, h, tid)] : make_float2(-__builtin_huge_valf(), 0.f);
+  float m = warp_max(ml.x);
+  if (lane == 0) s.wmax[warp] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) m = fmaxf(m, s.wmax[k]);
+  const float base = m == -__builtin_huge_valf() ? 0.f : m;
+  // a part of masked rows alone has l = 0; a NaN among its logits is a NaN in l
+  const float w = ml.y != 0.f ? ex2(ml.x - base) : 0.f;
+  s.weight[tid] = w;
+  float l = ml.y != 0.f ? w * ml.y : 0.f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (lane == 0) s.wsum[warp] = l;
+  __syncthreads();
+  l = 0.f;
+#pragma unroll
+  for (int k = 0; k < kWarps; ++k) l += s.wsum[k];
+  float4 acc[NC];
+#pragma unroll
+  for (int c = 0; c < NC; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = warp; k < parts; k += kWarps) {
+    float4 now[NC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) now[c] = x[0][c];
+    if (NC < 4) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c) x[0][c] = x[1][c];
+      request(x[1], k + 2 * kWarps);
+    } else {
+      request(x[0], k + kWarps);
+    }
+    const float wk = s.weight[k];
+    if (wk != 0.f) {  // a masked part's values are not looked at
+#pragma unroll
+      for (int c = 0; c < NC; ++c) add_part(acc[c], now[c], wk);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < NC; ++c) s.sums[warp][32 * c + lane] = acc[c];
+  __syncthreads();
+  if (tid >= 32 * NC) return;
+  float4 all = s.sums[0][tid];
+#pragma unroll
+  for (int t = 1; t < kWarps; ++t) add_part(all, s.sums[t][tid], 1.f);
+  store_head(P, join.y, h, 32 * c0 + tid, all, l, m);
+}
+
 // A unit's join is that of the query that starts in it and ends in a later one,
 // from the query's parts in the units' order.  The weights are e^(m_s - m) with m
 // the largest.  As many blocks as the SMs hold go through the joins, a team of a
 // block a head at a time; where there are so few joins (one long request: 74 parts
-// a head) that the blocks suffice for a head each, a block takes one head, its
-// warps every 16th part, and their sums are added in the warps' order.  Values are
-// requested before the maximum is known.  What bounds it: the parts, read once, and
-// below that the barriers and dependent loads of one item, 3 us (of 74 parts: by
-// teams 7).
+// a head) that the blocks suffice for a head or half a head each, a block takes one
+// with all its warps.  Values are requested before the maximum is known.  What
+// bounds it: the parts, read once, and below that the barriers and dependent loads
+// of one item, 3 us (of 74 parts: by teams 7).
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_join_kernel(const PagedAttnParams P) {
-  __shared__ int32_t units[kThreads];
-  __shared__ int32_t counts[kWarps];
-  __shared__ float weight[kThreads], wsum[kWarps], wmax[kWarps];
-  __shared__ float4 sums[kWarps][kTeam];
+  __shared__ JoinShared s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the first kernel may still run
-  // the units with a join, in order
-  const bool has = tid < P.units && P.joins[tid].x >= 0;
-  const uint32_t those = __ballot_sync(0xffffffffu, has);
-  if (lane == 0) counts[warp] = __popc(those);
+  const int2 mine = tid < P.units ? P.joins[tid] : make_int2(-1, -1);
+  const uint32_t those = __ballot_sync(0xffffffffu, mine.x >= 0);
+  if (lane == 0) s.counts[warp] = __popc(those);
   __syncthreads();
   int n = 0, at = __popc(those & ((1u << lane) - 1u));
 #pragma unroll
   for (int k = 0; k < kWarps; ++k) {
-    if (k < warp) at += counts[k];
-    n += counts[k];
+    if (k < warp) at += s.counts[k];
+    n += s.counts[k];
   }
-  if (has) units[at] = tid;
+  if (mine.x >= 0) s.list[at] = make_int4(tid, mine.x, mine.y, 0);
   __syncthreads();
-  const int items = n * P.H;
-  if (items <= static_cast<int>(gridDim.x)) {
-    const int item = blockIdx.x;
+  const int items = n * P.H, blocks = static_cast<int>(gridDim.x);
+  if (items <= blocks) {
+    const bool halves = 2 * items <= blocks;
+    const int item = halves ? blockIdx.x >> 1 : blockIdx.x;
     if (item >= items) return;
-    const int v = item / P.H, h = item - v * P.H, unit = units[v];
-    const int2 join = P.joins[unit];
-    const int parts = join.y - unit + 1;
-    float4 x[4];
-    auto request = [&](int k) {
-      const float4 *p = reinterpret_cast<const float4 *>(P.part_o + part_at(P, unit, h, min(k, parts - 1)) * kPagedDv);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) x[c] = p[32 * c + lane];
-    };
-    request(warp);
-    const float2 ml = tid < parts ? P.part_ml[part_at(P, unit, h, tid)] : make_float2(-__builtin_huge_valf(), 0.f);
-    float m = warp_max(ml.x);
-    if (lane == 0) wmax[warp] = m;
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) m = fmaxf(m, wmax[k]);
-    const float base = m == -__builtin_huge_valf() ? 0.f : m;
-    // a part of masked rows alone has l = 0; a NaN among its logits is a NaN in l
-    const float w = ml.y != 0.f ? ex2(ml.x - base) : 0.f;
-    weight[tid] = w;
-    float l = ml.y != 0.f ? w * ml.y : 0.f;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) wsum[warp] = l;
-    __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) l += wsum[k];
-    float4 acc[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = warp; k < parts; k += kWarps) {
-      float4 now[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) now[c] = x[c];
-      request(k + kWarps);
-      const float wk = weight[k];
-      if (wk != 0.f) {  // a masked part's values are not looked at
-#pragma unroll
-        for (int c = 0; c < 4; ++c) add_part(acc[c], now[c], wk);
-      }
+    const int v = item / P.H, h = item - v * P.H;
+    if (halves) {
+      join_wide<2>(P, s, s.list[v], h, 2 * (blockIdx.x & 1));
+    } else {
+      join_wide<4>(P, s, s.list[v], h, 0);
     }
-#pragma unroll
-    for (int c = 0; c < 4; ++c) sums[warp][32 * c + lane] = acc[c];
-    __syncthreads();
-    if (tid >= kTeam) return;
-    float4 all = sums[0][tid];
-#pragma unroll
-    for (int t = 1; t < kWarps; ++t) add_part(all, sums[t][tid], 1.f);
-    store_head(P, join.x, h, tid, all, l, m);
     return;
   }
   const int team = tid / kTeam, col = tid % kTeam;
-  for (int item = blockIdx.x * kTeams + team; item < items; item += gridDim.x * kTeams) {
-    const int v = item / P.H, h = item - v * P.H, unit = units[v];
-    const int2 join = P.joins[unit];
-    const int parts = join.y - unit + 1;
+  for (int item = blockIdx.x * kTeams + team; item < items; item += blocks * kTeams) {
+    const int v = item / P.H, h = item - v * P.H;
+    const int4 join = s.list[v];
+    const int unit = join.x, parts = join.z - unit + 1;
     float4 x[kBatch];
     float2 ml[kBatch];
     auto request = [&](int k0) {
@@ -152,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) paged_join_kernel(cons
         }
       }
     }
-    store_head(P, join.x, h, col, acc, l, m);
+    store_head(P, join.y, h, col, acc, l, m);
   }
 }
 

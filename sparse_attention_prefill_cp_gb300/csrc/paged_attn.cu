@@ -661,17 +661,22 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 }
 
 // How a call is divided: groups of 16, 32 or 64 heads, a CTA each per unit, and
-// as many units as fit the SMs (no more than there are blocks).
+// as many units as fit the SMs (no more than there are blocks).  As many heads to a
+// group as can be, since each group reads the rows; but where every block can have
+// an SM for each of smaller groups, those, whose block is shorter (one token of 128
+// heads over 1,024 rows: groups of 64 17.2 us, of 32 13.8, of 16 13.9; of 64 heads,
+// 16 requests of 128 rows: 12.6 against 10.7).
 struct PagedDivision {
   int group_heads, groups, units;
 };
 
 PagedDivision divide(int64_t n, int H, int max_pages, int nsel, int shift) {
-  PagedDivision d;
-  d.group_heads = H <= 16 ? 16 : H <= 32 ? 32 : 64;
+  const int64_t blocks = n * paged_blocks(INT32_MAX, nsel, max_pages, shift), sms = num_sms();
+  PagedDivision d{H <= 16 ? 16 : H <= 32 ? 32 : 64, 0, 0};
+  for (int g = 16; g < d.group_heads; g *= 2)
+    if (blocks * ((H + g - 1) / g) <= sms) d.group_heads = g;
   d.groups = (H + d.group_heads - 1) / d.group_heads;
-  const int64_t blocks = n * paged_blocks(INT32_MAX, nsel, max_pages, shift);
-  const int64_t fit = num_sms() / d.groups > 0 ? num_sms() / d.groups : 1;  // below the join's 512
+  const int64_t fit = sms / d.groups > 0 ? sms / d.groups : 1;  // below the join's 512
   d.units = static_cast<int>(blocks < fit ? blocks : fit);
   return d;
 }

@@ -17,9 +17,10 @@
 //
 // What bounds it: a group of four queries and 1,024 pages takes 31 K cycles, of
 // them 2 K to set up, 4 K to the first tile's MMA, 1.9 K a tile in the sums (1,024
-// of MMA; maxima run at half rate) and 8 K for the choice; a CTA fills an SM, so
-// nothing hides start and choice.  2,048 queries of 1,024 pages 64 us, 540 TFLOP/s;
-// 64 requests of 1,024 pages 10.6 us.
+// of MMA; each warp reads its query's weights from shared memory for every tile,
+// 1,024 cycles of it for 16 warps, and maxima run at half rate) and 8 K for the
+// choice; a CTA fills an SM, so nothing hides start and choice.  2,048 queries of
+// 1,024 pages 64 us, 540 TFLOP/s; 64 requests of 1,024 pages 10.5 us.
 #include "attn_common.cuh"
 #include "internal.h"
 
@@ -521,10 +522,10 @@ extern "C" dsa_status dsa_block_select(const void *q_idx, const float *w, int32_
   P.keep_last = keep_last;
   P.err = err;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // four queries share a request's keys where queries may share requests, once they fill the SMs (400 queries of 625
-  // blocks: 14 against 17 us); one query a CTA has two of them on an SM, or, where there are no more queries than SMs, a
-  // longer ring (64 of 1,024 blocks: 11 against 12 us)
-  if (req && n >= 2 * num_sms() && smem_bytes<SelCfg<4, 3>>(max_pages) <= kMaxSmem) return launch<SelCfg<4, 3>>(P, s);
+  // four queries share a request's keys where queries may share requests and there are more than fit the SMs at once,
+  // two CTAs of a query to an SM (625 blocks: 304 queries 13.5 against 12.1 us, 400 13.5 against 21.4); where there are
+  // no more queries than SMs a longer ring instead of a second CTA (64 of 1,024 blocks: 10.5 against 11.5 us)
+  if (req && n > 2 * num_sms() && smem_bytes<SelCfg<4, 3>>(max_pages) <= kMaxSmem) return launch<SelCfg<4, 3>>(P, s);
   if (n <= num_sms() && smem_bytes<SelCfg<1, 4>>(max_pages) <= kMaxSmem) return launch<SelCfg<1, 4>>(P, s);
   return launch<SelCfg<1, 2>>(P, s);
 }

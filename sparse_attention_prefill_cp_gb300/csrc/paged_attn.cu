@@ -108,7 +108,7 @@ __device__ __forceinline__ bool wg_or(int wg, bool p) {
 // A query counts a block more than it has, its first: what a segment costs beside
 // its blocks (Q, the first block's maxima, the result) is about a block's time, so
 // units of many short queries get fewer blocks (64 queries of 1 to 16 blocks and
-// 128 heads: 49 -> 37 us).
+// 128 heads: 49 -> 41 us).
 struct Walk {
   int q, j0, j1, nb, len, row;  // query, blocks [j0, j1) of its nb, positions it sees, its row of the table
   int take;                     // what the segment counts

@@ -9,18 +9,18 @@
 // pages at a time: pages as the M = 128 side of the MMA, (query, head) pairs as
 // N = 64 each, K = 128, so a page is a TMEM lane and the weighted sum over heads
 // is a thread's own loop.  Warps: sums, a warpgroup for each of four queries or two
-// that take the tiles of one by turns; MMA issue; four that gather the mean keys
-// by cp.async into a ring of tiles, page numbers a tile ahead.  Scores stay
+// that take the tiles of one by turns; MMA issue; two or four that gather the mean
+// keys by cp.async into a ring of tiles, page numbers a tile ahead.  Scores stay
 // in shared memory as order-preserving integers, from where the warps of a query
 // take them into registers, find the cut from counts and write the list in page
 // order.
 //
-// What bounds it: a group of four queries and 1,024 pages takes 31 K cycles, of
-// them 2 K to set up, 4 K to the first tile's MMA, 1.9 K a tile in the sums (1,024
-// of MMA; each warp reads its query's weights from shared memory for every tile,
-// 1,024 cycles of it for 16 warps, and maxima run at half rate) and 8 K for the
-// choice; a CTA fills an SM, so nothing hides start and choice.  2,048 queries of
-// 1,024 pages 64 us, 540 TFLOP/s; 64 requests of 1,024 pages 10.5 us.
+// What bounds it: a group of four queries and 1,024 pages takes 29 K cycles, of
+// them 2 K to set up, 4 K to the first tile's MMA, 1.7 K a tile in the sums (1,024
+// of MMA; a weight read from shared memory by a warp is 128 bytes into registers,
+// 1,024 cycles a tile where none are held: 64 us against 61, and maxima run at half
+// rate) and 8 K for the choice; a CTA fills an SM, so nothing hides start and
+// choice.  2,048 queries of 1,024 pages 61 us, 565 TFLOP/s; 64 requests 10.5 us.
 #include "attn_common.cuh"
 #include "internal.h"
 
@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kHI = 64, kDI = 128;
 constexpr int kRows = 128;                  // pages per tile
-constexpr int kLoadWarps = 4;
 constexpr int kChunkBytes = kRows * 128;    // 64 of the 128 dims (128B swizzle)
 constexpr int kTileBytes = 2 * kChunkBytes;
 
@@ -51,6 +50,9 @@ struct SelCfg {
   static constexpr int kBufs = 2;                   // accumulators
   static constexpr int kSumWarps = QT == 1 ? 8 : 16, kTeamWarps = kSumWarps / QT;
   static constexpr int kMmaWarp = kSumWarps, kFirstLoadWarp = kMmaWarp + 1;
+  static constexpr int kLoadWarps = QT == 1 ? 4 : 2;     // 19 warps leave a thread 96 registers, for most of its weights
+  static constexpr int kRead = QT == 1 ? 32 : 16;        // columns of an accumulator at a time
+  static constexpr int kHeldWeights = QT == 1 ? 0 : 48;  // of a query's 64 in registers, the others read for every tile
   static constexpr int kThreads = 32 * (kFirstLoadWarp + kLoadWarps);
   static constexpr int kOffQ = kStages * kTileBytes;
   static constexpr int kQChunk = N * 128;
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
   if (tid == 0) {
     misc[1] = misc[2] = misc[3] = 0;
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&k_full[s], kLoadWarps);
+      mbar_init(&k_full[s], C::kLoadWarps);
       mbar_init(&k_free[s], 1);
     }
     for (int b = 0; b < C::kBufs; ++b) {
@@ -314,9 +316,11 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
   bool ok = true;
   int tile = 0;
   if (warp >= C::kFirstLoadWarp) {
-    // ---------------- gather: warp w takes rows 8x + 2w + {0, 1} of a tile, x = 0..15, sixteen lanes a row; lane l
-    // knows the page of row 8 (l / 2) + 2w + l % 2.  A tile is handed on when the next one's copies are on their way.
-    const int w = warp - C::kFirstLoadWarp, u = lane & 15, my_row = 8 * (lane >> 1) + 2 * w + (lane & 1);
+    // ---------------- gather: warp w of W takes rows 2W x + 2w + {0, 1} of a tile, x = 0, 1, .., sixteen lanes a row;
+    // lane l knows the pages of its rows l, l + 32, .. in that order.  A tile is handed on when the next one's copies
+    // are on their way.
+    constexpr int W = C::kLoadWarps, kIds = kRows / W / 32;
+    const int w = warp - C::kFirstLoadWarp, u = lane & 15;
     const uint32_t to = smem_u32(smem) + (u >> 3) * kChunkBytes;
     bool landed = true;  // the tile before has been handed on
     auto land = [&](int t) {
@@ -326,14 +330,20 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
     };
     for (int q0 = 0; ok && q0 < QT;) {
       const Run r = run_at(q0);
+      int next[kIds];
       auto lookup = [&](int t) {
-        const int b = t * kRows + my_row;
-        return t < r.tiles && b < r.pages ? r.row[b] : -1;
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) {
+          const int at = 32 * k + lane, b = t * kRows + 2 * W * (at >> 1) + 2 * w + (at & 1);
+          next[k] = t < r.tiles && b < r.pages ? r.row[b] : -1;
+        }
       };
-      int next = lookup(0);
+      lookup(0);
       for (int t = 0; t < r.tiles; ++t, ++tile) {
-        const int page = next >= 0 && next < P.num_pages ? next : -1;
-        next = lookup(t + 1);
+        int page[kIds];
+#pragma unroll
+        for (int k = 0; k < kIds; ++k) page[k] = next[k] >= 0 && next[k] < P.num_pages ? next[k] : -1;
+        lookup(t + 1);
         const int s = tile % C::kStages;
         // no place for this tile yet: hand the one before on first
         if (!landed && !__all_sync(0xffffffffu, mbar_test(&k_free[s], ((tile / C::kStages) & 1) ^ 1))) {
@@ -344,8 +354,9 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
         ok = __all_sync(0xffffffffu, wait_for(&k_free[s], ((tile / C::kStages) & 1) ^ 1, failed, 93, tile));
         if (!ok) break;
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const int row = 8 * x + 2 * w + (lane >> 4), pg = __shfl_sync(0xffffffffu, page, 2 * x + (lane >> 4));
+        for (int x = 0; x < kRows / W / 2; ++x) {
+          const int row = 2 * W * x + 2 * w + (lane >> 4);
+          const int pg = __shfl_sync(0xffffffffu, page[x / 16], 2 * (x % 16) + (lane >> 4));
           cp_async_16(to + s * kTileBytes + row * 128 + (((u & 7) ^ (row & 7)) << 4),
                       P.keys + static_cast<int64_t>(max(pg, 0)) * (kDI / 8) + u, pg >= 0 ? 16u : 0u);
         }
@@ -392,6 +403,9 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + q * kHI;
     const float *wq = ws + q * kHI;
     const int have = misc[8 + q];
+    uint64_t held[C::kHeldWeights / 2 + 1];
+#pragma unroll
+    for (int k = 0; k < C::kHeldWeights / 2; ++k) held[k] = f2_pack(wq[2 * k], wq[2 * k + 1]);
     auto release = [&](int buf) {  // the accumulator is in registers
       tc_fence_before();
       __syncwarp();
@@ -414,16 +428,24 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
         if (mine) {
           uint64_t s[2] = {0, 0};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t x[32];
-            tmem_ld32(lane_base + buf * C::N + 32 * half, x);
+          for (int c = 0; c < kHI; c += C::kRead) {
+            uint32_t x[C::kRead];
+            tmem_ld(lane_base + buf * C::N + c, x);
             tmem_ld_wait();
-            if (half == 1) release(buf);
+            if (c == kHI - C::kRead) release(buf);
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              const float4 w4 = *reinterpret_cast<const float4 *>(wq + 32 * half + k);
-              s[0] = f2_fma(f2_pack(w4.x, w4.y), f2_pack(relu(x[k]), relu(x[k + 1])), s[0]);
-              s[1] = f2_fma(f2_pack(w4.z, w4.w), f2_pack(relu(x[k + 2]), relu(x[k + 3])), s[1]);
+            for (int k = 0; k < C::kRead; k += 4) {
+              uint64_t wa, wb;
+              if (c + k < C::kHeldWeights) {
+                wa = held[(c + k) / 2];
+                wb = held[(c + k) / 2 + 1];
+              } else {
+                const float4 w4 = *reinterpret_cast<const float4 *>(wq + c + k);
+                wa = f2_pack(w4.x, w4.y);
+                wb = f2_pack(w4.z, w4.w);
+              }
+              s[0] = f2_fma(wa, f2_pack(relu(x[k]), relu(x[k + 1])), s[0]);
+              s[1] = f2_fma(wb, f2_pack(relu(x[k + 2]), relu(x[k + 3])), s[1]);
             }
           }
           float s0, s1, s2, s3;

@@ -40,7 +40,10 @@ cudaError_t allow_smem(void (*kernel)(Params...), int bytes, std::atomic<uint64_
 }
 
 // Launch of a kernel that may become resident while the kernel before it in the
-// stream still runs: it touches memory only behind griddepcontrol.wait.
+// stream still runs: it touches memory only behind griddepcontrol.wait, and reads it
+// with plain loads.  A read-only load (__ldg, ld.global.nc) is for what nobody writes
+// while the kernel is there; it may be moved ahead of the wait and need not see what
+// the kernel before wrote.
 template <typename... Params, typename... Args>
 cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
                               const Args &...args) {

@@ -116,14 +116,14 @@ struct Walk {
   // the segment at count `o` of query `query`; false: the share is done
   __device__ __forceinline__ bool start(const PagedAttnParams &P, int query, int o) {
     for (q = query; q < P.n && left > 0; ++q, o = 0) {
-      len = __ldg(P.lens + q);
+      len = P.lens[q];
       nb = paged_blocks(len, P.nsel, P.max_pages, P.page_shift);
       if (nb == 0) continue;
       take = static_cast<int>(min(static_cast<int64_t>(nb + 1 - o), left));
       j0 = max(o - 1, 0);
       j1 = o + take - 1;
       if (j1 > j0) {
-        row = P.req ? __ldg(P.req + q) : q;
+        row = P.req ? P.req[q] : q;
         if (row < 0 || row >= P.batch) len = 0;  // reported by the loading warp
         return true;
       }
@@ -145,11 +145,11 @@ __device__ __forceinline__ int page_of(const PagedAttnParams &P, const Walk &w, 
   pos = INT32_MAX;
   if (P.blocks) {
     if (e >= P.nsel) return -1;
-    at = __ldg(P.blocks + static_cast<int64_t>(w.q) * P.nsel + e);
+    at = P.blocks[static_cast<int64_t>(w.q) * P.nsel + e];
   }
   if (at < 0 || at >= P.max_pages || static_cast<int64_t>(at) << P.page_shift >= w.len) return -1;
   pos = at << P.page_shift;
-  return __ldg(P.table + static_cast<int64_t>(w.row) * P.max_pages + at);
+  return P.table[static_cast<int64_t>(w.row) * P.max_pages + at];
 }
 
 template <class C>
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int i0 = min(tid * per, P.n), i1 = min(i0 + per, P.n);
   int64_t mine = 0;
   auto counts = [&](int i) {
-    const int nb = paged_blocks(__ldg(P.lens + i), P.nsel, P.max_pages, P.page_shift);
+    const int nb = paged_blocks(P.lens[i], P.nsel, P.max_pages, P.page_shift);
     return nb ? nb + 1 : 0;
   };
   for (int i = i0; i < i1; ++i) mine += counts(i);
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     int page_next = more ? lookup(walk.j0) : -1;
     while (ok && more) {
       if (walk.j0 == 0) {
-        const int len = __ldg(P.lens + walk.q), row = P.req ? __ldg(P.req + walk.q) : walk.q;
+        const int len = P.lens[walk.q], row = P.req ? P.req[walk.q] : walk.q;
         if (row < 0 || row >= P.batch || len > static_cast<int64_t>(P.max_pages) << P.page_shift) {
           bad[0] = 58;
           bad[1] = walk.q;

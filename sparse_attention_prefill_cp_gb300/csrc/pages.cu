@@ -276,7 +276,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) pages_append_kernel(const P
     uint4 x[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      if (u + 32 * k < A.kv_units) x[k] = __ldg(src + u + 32 * k);
+      if (u + 32 * k < A.kv_units) x[k] = src[u + 32 * k];
 #pragma unroll
     for (int k = 0; k < 3; ++k)
       if (u + 32 * k < A.kv_units) dst[u + 32 * k] = x[k];
@@ -284,14 +284,14 @@ __global__ void __launch_bounds__(kAppendWarps * 32) pages_append_kernel(const P
   if (!A.k_idx) return;
   const uint4 *const key = A.k_idx + static_cast<int64_t>(t) * A.key_units;
   uint4 *const page_keys = A.keys + (static_cast<int64_t>(page) << A.page_shift) * A.key_units;
-  if (lane < A.key_units) page_keys[static_cast<int64_t>(r) * A.key_units + lane] = __ldg(key + lane);
+  if (lane < A.key_units) page_keys[static_cast<int64_t>(r) * A.key_units + lane] = key[lane];
   if (r != P - 1) return;
   // which of the page's rows, t - (P - 1) .. t, are this call's: all that precede in its list as in the page
   uint32_t fresh[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int row = 32 * k + lane, tt = t - (P - 1 - row);
-    fresh[k] = __ballot_sync(0xffffffffu, row < P && tt >= 0 && __ldg(A.slots + max(tt, 0)) == slot - (P - 1 - row));
+    fresh[k] = __ballot_sync(0xffffffffu, row < P && tt >= 0 && A.slots[max(tt, 0)] == slot - (P - 1 - row));
   }
   const int half = lane >> 4, u = lane & 15;
   float sum[8];

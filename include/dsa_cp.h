@@ -691,8 +691,8 @@ dsa_status dsa_pages_slots(const int32_t *page_table, int32_t batch, int32_t max
  * of the page's P keys: fp32 sum, in an order that does not depend on which call
  * wrote which row, rounded once to bf16.  A negative slot leaves its row
  * unwritten; a slot beyond the pages is a DSA_ERR_DEVICE_BOUNDS and not
- * written.  The slots of a call are distinct, and those of one page stand
- * together, ascending and without gaps (as dsa_pages_slots makes them).
+ * written.  The slots of a call are distinct; their order does not matter (a page
+ * whose rows stand together, as dsa_pages_slots names them, is found fastest).
  */
 dsa_status dsa_pages_append(const void *kv, int64_t kv_stride, const void *k_idx, const int32_t *slots, int32_t n,
                             int32_t D, int32_t DI, void *cache, int64_t page_stride, int64_t row_stride,

@@ -845,8 +845,9 @@ def dsa_pages_append(kv: torch.Tensor, k_idx: torch.Tensor | None, slots: torch.
     written) of the paged ``cache`` bf16 [num_pages, P, D], and with ``k_idx``
     bf16 [n, DI] their index keys into ``key_cache`` [num_pages, P, DI] and
     the mean key of every page whose last row is written into ``block_keys``
-    [num_pages, DI].  Slots of one page stand together, ascending.  The rows
-    of kv and of cache may lie apart, each starting on a 16-byte boundary."""
+    [num_pages, DI].  Slots are distinct, in any order.  The rows of kv and
+    of cache may lie apart, each starting on a 16-byte boundary; k_idx and the
+    key caches are contiguous."""
     _result(binding().pages_append(kv, k_idx, slots, cache, key_cache, block_keys, stream), "dsa_pages_append")
 
 

@@ -252,81 +252,174 @@ struct PagesAppend {
 constexpr int kAppendWarps = 8;
 constexpr int kMaxKeyUnits = 16;  // half a warp
 
+constexpr int kAppendThreads = kAppendWarps * 32;
+constexpr int kShortList = 4 * kAppendThreads - 8;  // slots that a block holds, four a thread
+
+// A call's slots by fours, from the first 16-byte boundary on; the up to three ones
+// before it and behind the last four stand alone.
+struct SlotList {
+  const int32_t *slots;
+  int n, head, n4, rest;
+  __device__ __forceinline__ SlotList(const int32_t *s, int count) : slots(s), n(count) {
+    head = min(n, static_cast<int>((0 - (reinterpret_cast<uintptr_t>(s) >> 2)) & 3));
+    n4 = (n - head) >> 2;
+    rest = head + 4 * n4;
+  }
+  __device__ __forceinline__ int4 four(int k) const {
+    return k < n4 ? reinterpret_cast<const int4 *>(slots + head)[k] : make_int4(-1, -1, -1, -1);
+  }
+  // the ones that stand alone, x < 6
+  __device__ __forceinline__ int single_at(int x) const { return x < head ? x : rest + x - head; }
+  __device__ __forceinline__ int single(int x) const { return x < n - rest + head ? slots[single_at(x)] : -1; }
+};
+
 // Rows into their slots, a warp a row; the warp that writes a page's last row
-// makes the page's mean key.  The keys of the page's rows come from this call's
-// input as far as its tokens are the page's rows, else from the key cache; half
-// warp h sums rows h, h + 2, .. in fp32, and the halves are added, so a page's
-// key has the same bits however its rows arrived.  61 rows 3.5 us (a launch and
-// three dependent loads), 8,000 rows 5.8 us, 3.9 TB/s (a launch and its ramp).
-__global__ void __launch_bounds__(kAppendWarps * 32) pages_append_kernel(const PagesAppend A) {
-  const int t = static_cast<int>(blockIdx.x) * kAppendWarps + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (t >= A.n) return;
+// makes the page's mean key.  The keys of the page's rows that this call writes
+// come from its input, wherever in its list they stand (another warp may just be
+// writing them to the key cache), the others from the key cache; half warp h sums
+// rows h, h + 2, .. in fp32, and the halves are added, so a page's key has the same
+// bits however its rows arrived.  Where a page's rows stand: a block looks through
+// a short list, which its threads hold; in a longer one they are as a rule the P
+// rows up to the last, and only where they are not all there the block goes through
+// the list.  61 rows 3.5 us (a launch and three dependent loads), 8,000 rows 5.7 us,
+// 4.0 TB/s (a launch and its ramp).
+template <bool kShort>
+__global__ void __launch_bounds__(kAppendThreads) pages_append_kernel(const PagesAppend A) {
+  __shared__ int32_t places[kAppendWarps][128];  // of a page's rows in the list, -1: written before
+  __shared__ int4 sought[kAppendWarps / 4];      // the page whose rows a warp has to find, or -1
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp;
+  const SlotList list(A.slots, A.n);
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before may still run
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int slot = A.slots[t];
-  if (slot < 0) return;
-  const int page = slot >> A.page_shift, P = 1 << A.page_shift, r = slot & (P - 1);
-  if (page >= A.num_pages) {
-    if (lane == 0) record_error(A.err, DSA_ERR_DEVICE_BOUNDS, 56, t);
-    return;
+  int slot = t < A.n ? A.slots[t] : -1;
+  int4 held = make_int4(-1, -1, -1, -1);
+  int held1 = -1;
+  if (kShort && A.k_idx) {
+    held = list.four(tid);
+    held1 = list.single(tid);
   }
+  const int P = 1 << A.page_shift;
+  if (slot >> A.page_shift >= A.num_pages) {
+    if (lane == 0) record_error(A.err, DSA_ERR_DEVICE_BOUNDS, 56, static_cast<int>(t));
+    slot = -1;
+  }
+  const int page = slot >> A.page_shift, r = slot & (P - 1);
   const uint4 *src = A.kv + t * A.kv_stride;
-  uint4 *dst = A.cache + page * A.page_stride + r * A.row_stride;
-  for (int u = lane; u < A.kv_units; u += 96) {
-    uint4 x[3];
+  const bool has_key = A.k_idx && slot >= 0 && lane < A.key_units;
+  uint4 x[3];
+  auto load = [&](int u) {
 #pragma unroll
     for (int k = 0; k < 3; ++k)
-      if (u + 32 * k < A.kv_units) x[k] = src[u + 32 * k];
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      if (u + 32 * k < A.kv_units) dst[u + 32 * k] = x[k];
-  }
-  if (!A.k_idx) return;
-  const uint4 *const key = A.k_idx + static_cast<int64_t>(t) * A.key_units;
+      if (slot >= 0 && u + 32 * k < A.kv_units) x[k] = src[u + 32 * k];
+  };
+  load(lane);
+  uint4 key = make_uint4(0u, 0u, 0u, 0u);
+  if (has_key) key = A.k_idx[t * A.key_units + lane];
   uint4 *const page_keys = A.keys + (static_cast<int64_t>(page) << A.page_shift) * A.key_units;
-  if (lane < A.key_units) page_keys[static_cast<int64_t>(r) * A.key_units + lane] = key[lane];
-  if (r != P - 1) return;
-  // which of the page's rows, t - (P - 1) .. t, are this call's: all that precede in its list as in the page
-  uint32_t fresh[4];
+  auto store = [&]() {
+    if (slot < 0) return;
+    uint4 *dst = A.cache + page * A.page_stride + r * A.row_stride;
+    for (int u = lane; u < A.kv_units; u += 96) {
+      if (u != lane) load(u);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = 32 * k + lane, tt = t - (P - 1 - row);
-    fresh[k] = __ballot_sync(0xffffffffu, row < P && tt >= 0 && A.slots[max(tt, 0)] == slot - (P - 1 - row));
-  }
-  const int half = lane >> 4, u = lane & 15;
-  float sum[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) sum[k] = 0.f;
-  constexpr int kBatch = 8;
-#pragma unroll
-  for (int r0 = 0; r0 < 128; r0 += 2 * kBatch) {
-    if (r0 >= P) break;
-    uint4 x[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int row = r0 + 2 * k + half;
-      const uint4 *from = (fresh[r0 >> 5] >> (row & 31)) & 1u
-                              ? A.k_idx + static_cast<int64_t>(t - (P - 1 - row)) * A.key_units
-                              : page_keys + static_cast<int64_t>(row) * A.key_units;
-      x[k] = u < A.key_units ? from[u] : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < 3; ++k)
+        if (u + 32 * k < A.kv_units) dst[u + 32 * k] = x[k];
     }
+    if (has_key) page_keys[static_cast<int64_t>(r) * A.key_units + lane] = key;
+  };
+  if (A.k_idx) {
+    int32_t *const place = places[warp];
+    const bool ends = slot >= 0 && r == P - 1;
+    bool seek = ends;
+    if (!kShort && ends) {
+      bool here = true;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        sum[2 * e] += __uint_as_float(w[e] << 16);
-        sum[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+      for (int k = 0; k < 4; ++k) {
+        const int row = 32 * k + lane;
+        const int64_t tt = t - (P - 1 - row);
+        if (row < P) {
+          here = here && tt >= 0 && A.slots[tt] == slot - (P - 1 - row);
+          place[row] = static_cast<int>(tt);
+        }
       }
+      seek = !__all_sync(0xffffffffu, here);
+    }
+    if (!kShort) store();
+    if (seek)
+      for (int row = lane; row < P; row += 32) place[row] = -1;
+    if (lane == 0) reinterpret_cast<int32_t *>(sought)[warp] = seek ? page : -1;
+    if (__syncthreads_or(seek)) {
+      const int4 s0 = sought[0], s1 = sought[1];
+      const int wants[kAppendWarps] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+      for (int w = 0; w < kAppendWarps; ++w) {
+        const int want = wants[w];
+        if (want < 0) continue;
+        auto look = [&](int at, int s) {  // a slot below 0 has a page below 0
+          if (s >> A.page_shift == want) places[w][s & (P - 1)] = at;
+        };
+        auto look4 = [&](int k, const int4 &s) {
+          const int at = list.head + 4 * k;
+          look(at, s.x);
+          look(at + 1, s.y);
+          look(at + 2, s.z);
+          look(at + 3, s.w);
+        };
+        if (kShort) {
+          look4(tid, held);
+          look(list.single_at(tid), held1);
+        } else {
+          look(list.single_at(tid), list.single(tid));
+          constexpr int kBatch = 8;
+          for (int k0 = tid; k0 < list.n4; k0 += kBatch * kAppendThreads) {
+            int4 s[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) s[k] = list.four(k0 + kAppendThreads * k);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) look4(k0 + kAppendThreads * k, s[k]);
+          }
+        }
+      }
+      __syncthreads();
+    }
+    if (ends) {
+      const int half = lane >> 4, u = lane & 15;
+      float sum[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = 0.f;
+      constexpr int kBatch = 8;
+#pragma unroll
+      for (int r0 = 0; r0 < 128; r0 += 2 * kBatch) {
+        if (r0 >= P) break;
+        uint4 y[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const int row = r0 + 2 * k + half, at = place[row];
+          const uint4 *from = at >= 0 ? A.k_idx + static_cast<int64_t>(at) * A.key_units
+                                      : page_keys + static_cast<int64_t>(row) * A.key_units;
+          y[k] = u < A.key_units ? from[u] : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          const uint32_t w[4] = {y[k].x, y[k].y, y[k].z, y[k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            sum[2 * e] += __uint_as_float(w[e] << 16);
+            sum[2 * e + 1] += __uint_as_float(w[e] & 0xffff0000u);
+          }
+        }
+      }
+      const float inv = 1.f / static_cast<float>(P);  // a power of two
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[k] = (sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 16)) * inv;
+      if (half == 0 && u < A.key_units)
+        A.means[static_cast<int64_t>(page) * A.key_units + u] =
+            make_uint4(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]), pack_bf16x2(sum[4], sum[5]),
+                       pack_bf16x2(sum[6], sum[7]));
     }
   }
-  const float inv = 1.f / static_cast<float>(P);  // a power of two
-#pragma unroll
-  for (int k = 0; k < 8; ++k) sum[k] = (sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 16)) * inv;
-  if (half == 0 && u < A.key_units)
-    A.means[static_cast<int64_t>(page) * A.key_units + u] =
-        make_uint4(pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]), pack_bf16x2(sum[4], sum[5]),
-                   pack_bf16x2(sum[6], sum[7]));
+  if (kShort || !A.k_idx) store();
 }
 
 }  // namespace
@@ -414,8 +507,11 @@ extern "C" dsa_status dsa_pages_append(const void *kv, int64_t kv_stride, const 
   A.page_shift = shift;
   A.num_pages = num_pages;
   A.err = err;
+  // held lists: the keys are summed before the rows are stored, with 77 registers (61 rows: 3.5 against 5.0 us); where
+  // more than a block's threads hold, 52 registers and the rows' stores first (8,000 rows: 5.7 against 7.8 us)
+  const auto kernel = n <= kShortList ? pages_append_kernel<true> : pages_append_kernel<false>;
   const cudaError_t e =
-      launch_overlapped(pages_append_kernel, dim3(static_cast<unsigned>((n + kAppendWarps - 1) / kAppendWarps)),
-                        kAppendWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream), A);
+      launch_overlapped(kernel, dim3(static_cast<unsigned>((n + kAppendWarps - 1) / kAppendWarps)), kAppendThreads, 0,
+                        reinterpret_cast<cudaStream_t>(stream), A);
   return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }

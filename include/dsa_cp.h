@@ -729,8 +729,9 @@ dsa_status dsa_paged_attn_workspace_size(int32_t n, int32_t H, int32_t max_pages
  * MLA attention over the paged cache, for any number of queries down to one
  * token: query i (request req[i], or i where req is NULL: then n <= batch) sees
  * the positions p < lens[i] of its request, or with blocks those of them in the
- * pages blocks[i, :] (ordinals b of the request's pages; the used ones first,
- * distinct; a negative one ends the list), and for every head h
+ * pages blocks[i, :] (ordinals b of the request's pages, distinct, in any order;
+ * a negative one and one of a page that the query does not see name nothing), and
+ * for every head h
  *   l_p = softmax_scale * q[i, h, :] . k_p
  *   out[i, h, :] = sum_p e^(l_p - m) k_p[:Dv] / (sum_p e^(l_p - m) + e^(sink_h - m))
  *   q          bf16 [n][H][D];  out bf16 [n][H][Dv];  attn_sink fp32 [H] or NULL

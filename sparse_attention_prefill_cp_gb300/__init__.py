@@ -883,9 +883,10 @@ def dsa_paged_attn(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tenso
     Query i attends to the first ``lens``[i] positions of request ``req``[i]
     (None: request i) of ``page_table`` int32 [batch, max_pages], or with
     ``blocks`` int32 [n, nsel] to those of them in the pages that its row
-    names (ordinals of the request's pages, the used ones first, as
-    dsa_block_select makes them).  A length of 0 gives zeros, a negative one
-    leaves the query's rows of ``out`` as they are.  ``workspace``: uint8, at
+    names (ordinals of the request's pages, distinct, in any order; a negative
+    one and one of a page that the query does not see name nothing, so a list
+    may be shared).  A length of 0 gives zeros, a negative one leaves the
+    query's rows of ``out`` as they are.  ``workspace``: uint8, at
     least dsa_paged_attn_workspace_size bytes, allocated per call when
     omitted."""
     return _result(binding().paged_attn(q, cache, page_table, lens, softmax_scale, Dv, blocks, req, attn_sink, out,

@@ -147,14 +147,27 @@ struct Walk {
   __device__ __forceinline__ bool whole() const { return j0 == 0 && j1 == nb; }
 };
 
-// The page of entry e of a query's list and the entry's first position: the page
-// number unchecked, -1 (and no position) where the entry names none.
+// The page of entry e of what a query goes through, its list or its pages, and the
+// entry's first position: the page number unchecked, -1 (and no position) where the
+// entry names none.  Called by whole warps whose lanes' entries are of one block.
 __device__ __forceinline__ int page_of(const PagedAttnParams &P, const Walk &w, int e, int &pos) {
   int at = e;
   pos = INT32_MAX;
   if (P.blocks) {
-    if (e >= P.nsel) return -1;
-    at = load_plain(P.blocks + static_cast<int64_t>(w.q) * P.nsel + e);
+    const int32_t *list = P.blocks + static_cast<int64_t>(w.q) * P.nsel;
+    if (paged_listed(paged_pages(w.len, P.max_pages, P.page_shift), P.nsel)) {
+      if (e >= P.nsel) return -1;
+      at = load_plain(list + e);
+    } else {
+      // which of the block's up to eight pages the list names: a bit each
+      const uint32_t E = kRows >> P.page_shift, first = e & ~(E - 1);
+      uint32_t named = 0;
+      for (int k = threadIdx.x & 31; k < P.nsel; k += 32) {
+        const uint32_t d = static_cast<uint32_t>(load_plain(list + k)) - first;
+        if (d < E) named |= 1u << d;
+      }
+      if (!(__reduce_or_sync(0xffffffffu, named) >> (e - first) & 1u)) return -1;
+    }
   }
   if (at < 0 || at >= P.max_pages || static_cast<int64_t>(at) << P.page_shift >= w.len) return -1;
   pos = at << P.page_shift;

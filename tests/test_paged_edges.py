@@ -7,7 +7,7 @@ import torch
 
 import sparse_attention_prefill_cp_gb300 as dsa
 from conftest import ROOT
-from test_paged_gpu import D, gen, randn
+from test_paged_gpu import D, DV, INF, NAN, SCALE, attend64, bounds, gen, grid, i32, near, paged, randn
 
 CSRC = os.path.join(ROOT, "sparse_attention_prefill_cp_gb300", "csrc")
 
@@ -73,3 +73,42 @@ def test_rows_in_any_order_make_the_same_keys(P, rows):
                           (every[~half], every[half]), (every[~half].flip(0), every[half])):
         got = write(order, before)
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------ attention over chosen pages
+
+def attend_lists(lists, lens, have, P, H, req=None):
+    """The attention over these lists of pages against the one in 64 bits."""
+    cache, table, rows = paged(have, P, seed=P + H)
+    q, sink = randn(len(lens), H, D, seed=H), torch.randn(H, generator=gen(6))
+    blocks = torch.tensor(lists, dtype=torch.int32)
+    got = dsa.dsa_paged_attn(q.cuda(), cache, table, i32(lens), SCALE, DV, blocks=blocks.cuda(),
+                             req=None if req is None else i32(req), attn_sink=sink.cuda())
+    near(got, *attend64(q, rows, lens, req, lists, P, sink))
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P", [16, 128])
+@pytest.mark.parametrize("H", [16, 32, 128])
+def test_pages_that_a_query_does_not_see_name_nothing(P, H):
+    # more entries than pages: some of pages behind the query's last ahead of those that it sees, negative ones between
+    have = [10 * P] * 4
+    got = attend_lists([[3, 9, 8, 7, 6, 5, 4, 2, 1, 0, -1, -1], [9, 0, -1, 8, 1, -1, -1, 7, -5, 6, 2, 5],
+                        [-1] * 11 + [0], [4, -1, 3, -1, 2, 9, 8, 7, 6, -1, -1, 5]],
+                       [P - 3, 2 * P + 1, 1, 5 * P], have, P, H)
+    assert all(got[i].any() for i in range(4))
+    # as many entries as pages, or fewer
+    got = attend_lists([[9, 1], [-1, 2], [5, 0], [9, 8]], [2 * P, 3 * P, P - 1, 2 * P], have, P, H)
+    assert not got[3].any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("P,nsel", [(16, 70), (32, 33), (64, 9)])
+def test_a_list_shared_by_a_chunk(P, nsel):
+    # every query sees more than the one before, all have the same list, in falling order
+    n, have = 90, 70 * P + 5
+    pages = -(-have // P)
+    chosen = torch.randperm(pages, generator=gen(nsel))[:nsel].sort(descending=True).values.tolist()
+    lens = [1 + i * (have - 1) // (n - 1) for i in range(n)]
+    attend_lists([chosen] * n, lens, [have], P, 24, req=[0] * n)

@@ -711,7 +711,8 @@ dsa_status dsa_pages_append(const void *kv, int64_t kv_stride, const void *k_idx
  * With at most nsel pages all are taken.  A NaN score ranks below every number.
  * A negative lens[i] is no query: its row of blocks keeps its values.  A request
  * or length that the table does not have, and a page number that is none, are
- * DSA_ERR_DEVICE_BOUNDS (such a page ranks last).  A query's scores are kept in
+ * DSA_ERR_DEVICE_BOUNDS (such a page ranks last, behind NaN scores, but is taken
+ * where it is one of the first and last ones or all are).  A query's scores are kept in
  * shared memory: max_pages up to 37,000 (DSA_ERR_UNSUPPORTED beyond).
  */
 dsa_status dsa_block_select(const void *q_idx, const float *w, int32_t n, int32_t HI, int32_t DI,

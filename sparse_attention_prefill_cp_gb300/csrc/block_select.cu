@@ -73,13 +73,14 @@ __device__ __forceinline__ float relu(uint32_t x) {
   return y;
 }
 
-// Scores to integers of the same order; a NaN is below every number, 0 is kept
-// for pages that do not take part.
+// Scores to integers of the same order, from that of -inf (0x7fffff) up; a NaN is
+// below every number and a page that is none below a NaN; 0 is kept for what does
+// not take part, all bits for the pages that are always taken.
+constexpr uint32_t kKeyNoPage = 1, kKeyNaN = 2, kKeyForced = 0xffffffffu;
 __device__ __forceinline__ uint32_t ordered(float s) {
-  if (!(s == s)) return 1u;
+  if (!(s == s)) return kKeyNaN;
   const uint32_t u = __float_as_uint(s + 0.f);  // -0 is 0
-  const uint32_t k = u & 0x80000000u ? ~u : u | 0x80000000u;
-  return max(k, 2u);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
 // Barrier among the warps of a team.
@@ -453,11 +454,11 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
           f2_unpack(s[1], s2, s3);
           uint32_t key = ordered((s0 + s1) + (s2 + s3));
           if (page < 0 || page >= P.num_pages) {
-            key = 1u;
+            key = kKeyNoPage;
             bad[0] = 57;
             bad[1] = i0 + q;
           }
-          if (b < P.keep_first || b >= have - P.keep_last) key = 0xffffffffu;
+          if (b < P.keep_first || b >= have - P.keep_last) key = kKeyForced;
           keys[q * ld + b] = key;
         } else {
           release(buf);
@@ -474,6 +475,12 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
   }
   if (warp < C::kSumWarps && ok) {
     const int q = warp / C::kTeamWarps, i = i0 + q;
+    if (misc[8 + q] <= P.nsel) {
+      // all its pages are taken; those that no tile was scored for are looked at here
+      const int32_t *row = P.table + static_cast<int64_t>(max(misc[4 + q], 0)) * P.max_pages;
+      for (int k = (warp % C::kTeamWarps) * 32 + lane; k < misc[8 + q]; k += C::kTeamWarps * 32)
+        if (row[k] < 0 || row[k] >= P.num_pages) record_error(P.err, DSA_ERR_DEVICE_BOUNDS, 57, i);
+    }
     if (i < P.n && P.lens[i] >= 0)
       choose<C::kTeamWarps>(keys + q * ld, misc[8 + q], P.nsel, q, warp % C::kTeamWarps, lane, misc + 16,
                             reinterpret_cast<uint32_t *>(smem), P.out + static_cast<int64_t>(i) * P.nsel);

@@ -112,3 +112,62 @@ def test_a_list_shared_by_a_chunk(P, nsel):
     chosen = torch.randperm(pages, generator=gen(nsel))[:nsel].sort(descending=True).values.tolist()
     lens = [1 + i * (have - 1) // (n - 1) for i in range(n)]
     attend_lists([chosen] * n, lens, [have], P, 24, req=[0] * n)
+
+
+# ------------------------------------------------------------------ choosing among pages that are none
+
+def select(lens, table, keys, nsel, q=None, w=None, **kw):
+    n = len(lens)
+    q = grid(n, 64, 128, std=1, step=0.25, seed=2) if q is None else q
+    w = grid(n, 64, std=0.125, step=1 / 32, seed=3).abs() if w is None else w
+    return dsa.dsa_block_select(q.to(torch.bfloat16).cuda(), w.cuda(), keys.to(torch.bfloat16).cuda(), table.cuda(),
+                                i32(lens), 16, nsel, **kw)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("page", [-1, 40])
+@pytest.mark.parametrize("queries", [1, 400])
+def test_a_page_that_is_none_is_reported_where_all_are_taken(page, queries):
+    # no more pages than a list takes, so none is scored; alone, and among queries that share the request
+    width, nsel = 6, 8
+    keys = grid(40, 128, std=0.5, step=1 / 32, seed=4)
+    table = torch.arange(2 * width, dtype=torch.int32).view(2, width)
+    req = [0] * (queries // 2) + [1] * (queries - queries // 2)
+    lens, want = [16 * width - 3] * queries, i32([0, 1, 2, 3, 4, 5, -1, -1])
+    got = select(lens, table, keys, nsel, req=i32(req))
+    dsa.dsa_poll_device_error()
+    assert (got == want).all()
+    table[1, 4] = page
+    select([16 * 4] * queries, table, keys, nsel, req=i32(req))
+    dsa.dsa_poll_device_error()                      # behind what the queries see
+    got = select(lens, table, keys, nsel, req=i32(req))
+    assert bounds(57) >= queries // 2
+    assert (got == want).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("queries", [1, 400])
+def test_a_page_that_is_none_ranks_behind_scores_that_are_no_numbers(queries):
+    width, nsel = 12, 6
+    keys = grid(40, 128, std=0.5, step=1 / 32, seed=4)
+    keys[5:width - 1] = NAN                          # of pages 1 .. 10 four have a score
+    table = torch.arange(width, dtype=torch.int32)[None].clone()
+    table[0, 1:4] = torch.tensor([-1, 40, -7])       # pages 1 to 3 are none: one score is left
+    got = select([16 * width] * queries, table, keys, nsel, req=i32([0] * queries))
+    bounds(57)
+    assert (got == i32([0, 4, 5, 6, 7, 11])).all()
+
+
+@pytest.mark.gpu
+def test_forced_pages_are_taken_whatever_they_are():
+    width, nsel = 12, 4
+    keys = grid(40, 128, std=0.5, step=1 / 32, seed=4)
+    table = torch.arange(width, dtype=torch.int32)[None].clone()
+    table[0, 0] = 40
+    keys[11] = NAN
+    got = select([16 * width], table, keys, nsel)
+    assert bounds(57) == 0
+    q, w = grid(1, 64, 128, std=1, step=0.25, seed=2), grid(1, 64, std=0.125, step=1 / 32, seed=3).abs()
+    score = (w[0].double()[:, None] * (q[0].double() @ keys[:width].double().T).clamp(min=0)).sum(0)
+    best = sorted(range(1, 11), key=lambda b: (-score[b].item(), b))[:2]
+    assert got[0].tolist() == [0] + sorted(best) + [11]

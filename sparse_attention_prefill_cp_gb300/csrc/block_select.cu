@@ -434,6 +434,11 @@ __global__ void __launch_bounds__(C::kThreads) block_select_kernel(const SelectP
             tmem_ld(lane_base + buf * C::N + c, x);
             tmem_ld_wait();
             if (c == kHI - C::kRead) release(buf);
+            if (P.HI < kHI) {  // heads that are none: a zero row of Q, but 0 * inf is no number
+#pragma unroll
+              for (int k = 0; k < C::kRead; ++k)
+                if (c + k >= P.HI) x[k] = 0u;
+            }
 #pragma unroll
             for (int k = 0; k < C::kRead; k += 4) {
               uint64_t wa, wb;

@@ -171,3 +171,27 @@ def test_forced_pages_are_taken_whatever_they_are():
     score = (w[0].double()[:, None] * (q[0].double() @ keys[:width].double().T).clamp(min=0)).sum(0)
     best = sorted(range(1, 11), key=lambda b: (-score[b].item(), b))[:2]
     assert got[0].tolist() == [0] + sorted(best) + [11]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("queries", [3, 400])
+@pytest.mark.parametrize("HI", [1, 5, 16, 33, 48, 63, 64])
+def test_infinite_keys_with_any_number_of_index_heads(HI, queries):
+    # the score of a page with an infinite key is infinite (or no number), whatever the number of heads
+    width, nsel = 150, 5
+    keys = grid(width, 128, std=0.5, step=1 / 32, seed=4)
+    q = grid(1, HI, 128, std=1, step=0.25, seed=2)
+    q[0, :, 7] = 1.0
+    w = grid(1, HI, std=0.125, step=1 / 32, seed=3).abs() + 1 / 32
+    keys[9, 7], keys[140, 7] = INF, INF              # the highest scores
+    keys[3, 7] = -INF                                # relu(-inf) = 0: the lowest
+    q[0, 0, 8] = 0.0
+    keys[11, 8] = INF                                # 0 * inf: no number
+    s = (w[0].double()[:, None] * (q[0].double() @ keys.double().T).clamp(min=0)).sum(0)
+    assert s[9] == s[140] == INF and s[3] == 0 and torch.isnan(s[11])
+    rest = sorted((b for b in range(1, width - 1) if not torch.isnan(s[b])), key=lambda b: (-s[b].item(), b))
+    want = sorted([0, width - 1] + rest[:nsel - 2])
+    table = torch.arange(width, dtype=torch.int32)[None]
+    got = select([16 * width] * queries, table, keys, nsel, q=q.expand(queries, -1, -1).contiguous(),
+                 w=w.expand(queries, -1).contiguous(), req=i32([0] * queries))
+    assert (got == i32(want)).all()

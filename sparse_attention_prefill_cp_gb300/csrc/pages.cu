@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kSlotThreads)
   const int tid = threadIdx.x, lane = tid & 31;
   // of a request: its first position and how many it has (none below 0)
   auto begin = [&](int r) { return first ? max(first[r], 0) : 0; };
-  auto count = [&](int r) { return max(seq[r] - begin(r), 0); };
+  auto count = [&](int r) { return max(max(seq[r], 0) - begin(r), 0); };
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the kernel before may still run
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   int64_t start = 0;

@@ -195,3 +195,15 @@ def test_infinite_keys_with_any_number_of_index_heads(HI, queries):
     got = select([16 * width] * queries, table, keys, nsel, q=q.expand(queries, -1, -1).contiguous(),
                  w=w.expand(queries, -1).contiguous(), req=i32([0] * queries))
     assert (got == i32(want)).all()
+
+
+# ------------------------------------------------------------------ lengths that are no lengths
+
+@pytest.mark.gpu
+def test_a_length_below_zero_counts_as_zero_whatever_the_first_position():
+    table = i32([[0, 1], [2, 3], [4, 5]])
+    for first, length in ((2 ** 31 - 1, -2), (2 ** 31 - 1, -2 ** 31), (1, -2 ** 31), (-2 ** 31, -2 ** 31), (2 ** 31 - 1, 5)):
+        got = dsa.dsa_pages_slots(table, i32([0, first, 1]), i32([2, length, 3]), 16, 6).tolist()
+        if length < 0 or first < 0:
+            assert bounds(52) == 1
+        assert got == [0, 1, 65, 66, -1, -1]

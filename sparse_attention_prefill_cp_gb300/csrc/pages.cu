@@ -511,7 +511,7 @@ extern "C" dsa_status dsa_pages_append(const void *kv, int64_t kv_stride, const 
   // more than a block's threads hold, 52 registers and the rows' stores first (8,000 rows: 5.7 against 7.8 us)
   const auto kernel = n <= kShortList ? pages_append_kernel<true> : pages_append_kernel<false>;
   const cudaError_t e =
-      launch_overlapped(kernel, dim3(static_cast<unsigned>((n + kAppendWarps - 1) / kAppendWarps)), kAppendThreads, 0,
+      launch_overlapped(kernel, dim3(static_cast<unsigned>((n + int64_t{kAppendWarps - 1}) / kAppendWarps)), kAppendThreads, 0,
                         reinterpret_cast<cudaStream_t>(stream), A);
   return e == cudaSuccess ? check_launch() : cuda_fail(e);
 }

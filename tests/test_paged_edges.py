@@ -207,3 +207,23 @@ def test_a_length_below_zero_counts_as_zero_whatever_the_first_position():
         if length < 0 or first < 0:
             assert bounds(52) == 1
         assert got == [0, 1, 65, 66, -1, -1]
+
+
+@pytest.mark.gpu
+def test_as_many_rows_as_a_call_may_have():
+    # 2^31 - 1 rows, of which four have a slot
+    n, P = 2 ** 31 - 1, 16
+    if torch.cuda.mem_get_info()[0] < 50 << 30:
+        pytest.skip("needs 50 GB")
+    kv = torch.empty(n, 8, dtype=torch.bfloat16, device="cuda")
+    slots = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    cache = torch.zeros(2, P, 8, dtype=torch.bfloat16, device="cuda")
+    want = torch.zeros(2, P, 8, dtype=torch.bfloat16)
+    for k, (at, slot) in enumerate(((0, 3), (7, 17), (n - 8, 31), (n - 1, 0))):
+        x = randn(8, seed=k)
+        kv[at], slots[at] = x.cuda(), slot
+        want.view(-1, 8)[slot] = x
+    dsa.dsa_pages_append(kv, None, slots, cache)
+    assert torch.equal(cache.cpu(), want)
+    del kv, slots
+    torch.cuda.empty_cache()

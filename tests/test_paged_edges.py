@@ -227,3 +227,34 @@ def test_as_many_rows_as_a_call_may_have():
     assert torch.equal(cache.cpu(), want)
     del kv, slots
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ the example of a step
+
+@pytest.mark.gpu
+def test_the_example_of_a_step_gives_back_every_page():
+    """README's example as it stands: after its last call the pages of the requests that stay and the free ones are all
+    there are."""
+    text = open(os.path.join(ROOT, "README.md"), encoding="utf-8").read()
+    code = next(b for b in text.split("```python\n")[1:] if "dsa_pages_update" in b).split("```")[0]
+    batch, P, num_pages, max_pages = 4, 64, 40, 8
+    held, new, left = [0, 63, 64, 130], [100, 64, 65, 131], [0, 64, 0, 131]
+    rows = sum(new) - sum(held)
+    req = [b for b in range(batch) for _ in range(new[b] - held[b])]
+    seen = [p + 1 for b in range(batch) for p in range(held[b], new[b])]
+    bf16 = lambda *shape, seed: randn(*shape, seed=seed).cuda()
+    at = code.index("dsa.dsa_pages_update")
+    env = dict(torch=torch, dsa=dsa, batch=batch, num_pages=num_pages, max_pages=max_pages, new_rows=rows,
+               held_lens=i32(held), seq_lens=i32(new), remaining_lens=i32(left), lens=i32(seen), req=i32(req),
+               kv=bf16(rows, D, seed=1), k_idx=bf16(rows, 128, seed=2), q=bf16(rows, 128, D, seed=3),
+               q_idx=bf16(rows, 64, 128, seed=4), w=torch.randn(rows, 64, device="cuda"), sink=torch.zeros(128, device="cuda"))
+    exec(code[:at], env)
+    zero = i32([0] * batch)
+    dsa.dsa_pages_update(env["table"], zero, env["held_lens"], env["free"], env["count"], P)
+    for name in ("cache", "key_cache", "block_keys"):
+        env[name].zero_()
+    exec(code[at:], env)
+    dsa.dsa_poll_device_error()
+    owned = [page for row, n in zip(env["table"].tolist(), left) for page in row[:-(-n // P)]]
+    assert sorted(owned + env["free"].tolist()[:env["count"].item()]) == list(range(num_pages))
+    assert (env["table"] >= 0).sum().item() == len(owned)

@@ -5,7 +5,7 @@ from __future__ import annotations
 import ctypes as C
 import os
 
-from .build import BINDING_PATH, LIB_PATH
+from .build import LIB_PATH, binding_path
 
 c_stream = C.c_void_p
 c_i32p = C.POINTER(C.c_int32)
@@ -156,16 +156,18 @@ _BINDING = None
 
 
 def binding():
-    """The native binding of the calls of a decode step (csrc/binding.cpp);
-    built first if it is missing.  Raises if it cannot be built or loaded."""
+    """The native binding of the calls of a decode step (csrc/binding.cpp), of
+    this Python and this torch; built first if it is missing.  Raises if it
+    cannot be built or loaded."""
     global _BINDING
     if _BINDING is None:
         load()
-        if not os.path.exists(BINDING_PATH):
-            from .build import build
-            build()
+        path = binding_path()
+        if not os.path.exists(path):
+            from .build import build_binding
+            build_binding()
         import importlib.util
-        spec = importlib.util.spec_from_file_location(__package__ + "._binding", BINDING_PATH)
+        spec = importlib.util.spec_from_file_location(__package__ + "._binding", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
         _BINDING = module

@@ -2,8 +2,10 @@
 binding of the calls of a decode step (csrc/binding.cpp) with g++.
 
 Every csrc/*.cu compiles to an object in parallel, then nvcc links the
-shared library next to this file, and g++ the binding against it.  Objects go to ``_build/`` at the repo
-root (git-ignored).  ``python -m sparse_attention_prefill_cp_gb300.build``
+shared library next to this file, and g++ the binding against it.  The library
+needs nvcc alone: it is there whether or not the binding, which needs the
+headers of torch and of Python, can be built.  Objects go to ``_build/`` at
+the repo root (git-ignored).  ``python -m sparse_attention_prefill_cp_gb300.build``
 runs it from the command line.
 """
 from __future__ import annotations
@@ -21,7 +23,6 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "libdsa_cp.so")
-BINDING_PATH = os.path.join(PKG_DIR, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -48,6 +49,21 @@ def cuda_home() -> str:
     return os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
 
 
+def binding_tag() -> str:
+    """The Python and the torch that a binding is for; both are in its file's name, so that after a change of either it is
+    built again instead of loaded."""
+    import torch
+    return f"{sys.implementation.cache_tag}-torch{torch.__version__}"
+
+
+def binding_path() -> str:
+    return os.path.join(PKG_DIR, f"_binding.{binding_tag()}.so")
+
+
+def binding_object() -> str:
+    return os.path.join(BUILD_DIR, f"binding.{binding_tag()}.o")
+
+
 def binding_commands(src: str, obj: str, target: str) -> tuple[list, list]:
     """The compiler's and the linker's command of the Python binding."""
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
@@ -57,7 +73,7 @@ def binding_commands(src: str, obj: str, target: str) -> tuple[list, list]:
                os.path.join(cuda_home(), "include")]
     compile_cmd = [gxx, "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", "-c", src, "-o", obj] + \
         ["-I" + d for d in include]
-    link_cmd = [gxx, "-shared", "-o", target, obj, "-L" + PKG_DIR, "-l:" + os.path.basename(LIB_PATH),
+    link_cmd = [gxx, "-shared", "-o", target, obj, "-L" + os.path.dirname(LIB_PATH), "-l:" + os.path.basename(LIB_PATH),
                 "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
                 "-lc10_cuda"]
     return compile_cmd, link_cmd
@@ -74,28 +90,19 @@ def _stale(target: str, deps: list) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
-    """Compile (when sources changed) and return the path of libdsa_cp.so."""
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    headers = glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+def _headers() -> list:
+    return glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(ROOT, "include", "*.h"))
-    objs, procs = [], []
-    for src in sources():
-        obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
-        objs.append(obj)
-        if force or _stale(obj, [src] + headers):
-            cmd = [nvcc()] + NVCC_FLAGS + SOURCE_FLAGS.get(os.path.basename(src), []) + list(extra_flags) + \
-                ["-c", src, "-o", obj]
-            if verbose:
-                print(" ".join(cmd), flush=True)
-            procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    src = os.path.join(CSRC, "binding.cpp")
-    binding_obj, tmp_binding = os.path.join(BUILD_DIR, "binding.o"), BINDING_PATH + ".tmp"
-    compile_binding, link_binding = binding_commands(src, binding_obj, tmp_binding)
-    if force or _stale(binding_obj, [src] + headers):
-        if verbose:
-            print(" ".join(compile_binding), flush=True)
-        procs.append((src, subprocess.Popen(compile_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+
+
+def _start(cmd: list, verbose: bool) -> subprocess.Popen:
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+
+
+def _finish(procs: list, verbose: bool) -> None:
+    """Wait for the compilers of (source, process); raise what the failed ones said."""
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -104,25 +111,64 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         elif verbose and out:
             print(out.decode(errors="replace"), flush=True)
     if failed:
-        msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"the compiler failed:\n{msg}")
-    if force or procs or _stale(LIB_PATH, objs):
-        tmp = LIB_PATH + ".tmp"
-        cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs
-        if verbose:
-            print(" ".join(cmd), flush=True)
-        r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        if r.returncode != 0:
-            raise RuntimeError("nvcc link failed:\n" + r.stdout.decode(errors="replace"))
-        os.replace(tmp, LIB_PATH)
-    if force or procs or _stale(BINDING_PATH, [binding_obj, LIB_PATH]):
-        if verbose:
-            print(" ".join(link_binding), flush=True)
-        r = subprocess.run(link_binding, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-        if r.returncode != 0:
-            raise RuntimeError("linking the binding failed:\n" + r.stdout.decode(errors="replace"))
-        os.replace(tmp_binding, BINDING_PATH)
+        raise RuntimeError("the compiler failed:\n" + "\n".join(f"--- {s}\n{o}" for s, o in failed))
+
+
+def _link(cmd: list, tmp: str, target: str, verbose: bool) -> None:
+    _finish([(target, _start(cmd, verbose))], verbose)
+    os.replace(tmp, target)
+
+
+def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
+    """Compile (when sources changed) and return the path of libdsa_cp.so; with
+    torch there, the binding too."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    headers = _headers()
+    objs, procs = [], []
+    for src in sources():
+        obj = os.path.join(BUILD_DIR, os.path.basename(src)[:-3] + ".o")
+        objs.append(obj)
+        if force or _stale(obj, [src] + headers):
+            procs.append((src, _start([nvcc()] + NVCC_FLAGS + SOURCE_FLAGS.get(os.path.basename(src), []) +
+                                      list(extra_flags) + ["-c", src, "-o", obj], verbose)))
+    binding = compile_binding(verbose, force) if importlib.util.find_spec("torch") is not None else None
+    try:
+        _finish(procs, verbose)
+        if force or procs or _stale(LIB_PATH, objs):
+            tmp = LIB_PATH + ".tmp"
+            _link([nvcc()] + ARCH + ["-shared", "-o", tmp] + objs, tmp, LIB_PATH, verbose)
+    except BaseException:
+        for _, p in binding or []:
+            p.communicate()
+        raise
+    if binding is not None:
+        link_binding(binding, verbose, force)
     return LIB_PATH
+
+
+def compile_binding(verbose: bool = False, force: bool = False) -> list:
+    """Start the binding's compiler where its object is not up to date: [(source, process)] or []."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not (force or _stale(binding_object(), [src] + _headers())):
+        return []
+    return [(src, _start(binding_commands(src, binding_object(), "")[0], verbose))]
+
+
+def link_binding(compiling: list, verbose: bool = False, force: bool = False) -> str:
+    """Wait for the binding's compiler and link the binding against the library as it is."""
+    _finish(compiling, verbose)
+    target, obj = binding_path(), binding_object()
+    if force or compiling or _stale(target, [obj]):
+        tmp = target + ".tmp"
+        _link(binding_commands("", obj, tmp)[1], tmp, target, verbose)
+    return target
+
+
+def build_binding(verbose: bool = False, force: bool = False) -> str:
+    """The binding alone.  The library is left as it is: a process that has loaded it would load a rebuilt one beside it,
+    with an error record of its own."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    return link_binding(compile_binding(verbose, force), verbose, force)
 
 
 if __name__ == "__main__":

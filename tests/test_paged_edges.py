@@ -7,9 +7,12 @@ import torch
 
 import sparse_attention_prefill_cp_gb300 as dsa
 from conftest import ROOT
+from oracle import dsa_oracle as O
+from sparse_attention_prefill_cp_gb300 import _lib
 from test_paged_gpu import D, DV, INF, NAN, SCALE, attend64, bounds, gen, grid, i32, near, paged, randn
 
 CSRC = os.path.join(ROOT, "sparse_attention_prefill_cp_gb300", "csrc")
+A = 0x10000     # an aligned address, never read
 
 
 @pytest.fixture(autouse=True)
@@ -258,3 +261,119 @@ def test_the_example_of_a_step_gives_back_every_page():
     owned = [page for row, n in zip(env["table"].tolist(), left) for page in row[:-(-n // P)]]
     assert sorted(owned + env["free"].tolist()[:env["count"].item()]) == list(range(num_pages))
     assert (env["table"] >= 0).sum().item() == len(owned)
+
+
+# ------------------------------------------------------------------ every kernel that a call may take
+
+def oracle_choice(i, q, w, keys, row, length, P, nsel):
+    return O.block_select(q[i].numpy(), w[i].numpy(), keys.numpy(), row, length, P, nsel)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n,shared,width", [(152, False, 40), (153, False, 40), (200, False, 200), (304, True, 40),
+                                            (700, False, 130), (320, True, 4097), (320, True, 4096)])
+def test_selection_of_many_requests_and_of_wide_tables(n, shared, width):
+    # up to an SM each, two to an SM, more than that with a request each; queries that share requests in tables too wide
+    # for groups of four
+    P, nsel, pages = 16, 9, 600
+    requests = 3 if shared else n
+    g = gen(n + width)
+    table = torch.randint(0, pages, (requests, width), generator=g, dtype=torch.int32)
+    req = [i * 3 // n for i in range(n)] if shared else list(range(n))
+    lens = torch.randint(0, min(width, 300) * P + 1, (n,), generator=g).tolist()
+    lens[0], lens[1], lens[2], lens[n - 1] = 0, -1, width * P, 1
+    q, w = grid(n, 64, 128, std=1, step=0.25, seed=2), grid(n, 64, std=0.125, step=1 / 32, seed=3)
+    keys = grid(pages, 128, std=0.5, step=1 / 32, seed=4)
+    out = torch.full((n, nsel), -9, dtype=torch.int32, device="cuda")
+    dsa.dsa_block_select(q.to(torch.bfloat16).cuda(), w.cuda(), keys.to(torch.bfloat16).cuda(), table.cuda(), i32(lens), P,
+                         nsel, req=i32(req) if shared else None, out=out)
+    got = out.tolist()
+    for i in sorted({*range(0, n, 7), 1, 2, n - 2, n - 1}):
+        want = [-9] * nsel if lens[i] < 0 else oracle_choice(i, q, w, keys, table[req[i]].tolist(), lens[i], P, nsel)
+        assert got[i] == want, i
+
+
+def widest_table():
+    """The most pages of a request that a selection takes, from the host's own check."""
+    lib = _lib.load()
+    takes = lambda width: lib.dsa_block_select(A, A, 0, 64, 128, A, 8, 16, A, 1, width, A, None, 4, 1, 1, A, None) == 0
+    lo, hi = 1, 1 << 17
+    assert takes(lo) and not takes(hi)
+    while hi - lo > 1:
+        mid = (lo + hi) // 2
+        lo, hi = (mid, hi) if takes(mid) else (lo, mid)
+    return lo
+
+
+def test_the_widest_table_is_what_the_header_says():
+    assert 37000 <= widest_table() < 40000
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [1, 5])
+def test_selection_of_the_widest_table(n):
+    width, P, nsel, pages = widest_table(), 16, 64, 5000
+    table = torch.randint(0, pages, (1, width), generator=gen(1), dtype=torch.int32)
+    q, w = grid(n, 64, 128, std=1, step=0.25, seed=2), grid(n, 64, std=0.125, step=1 / 32, seed=3)
+    keys = grid(pages, 128, std=0.5, step=1 / 32, seed=4)
+    lens = [width * P - i * 40000 for i in range(n)]
+    got = dsa.dsa_block_select(q.to(torch.bfloat16).cuda(), w.cuda(), keys.to(torch.bfloat16).cuda(), table.cuda(),
+                               i32(lens), P, nsel, req=i32([0] * n))
+    for i in range(n):
+        assert got[i].tolist() == oracle_choice(i, q, w, keys, table[0].tolist(), lens[i], P, nsel), i
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [64, 128])
+def test_steps_over_a_wide_table(H):
+    """Steps of a batch whose table is as wide as long requests need, so that the heads stay in groups of 64: each step
+    against 64 bits, and captured and replayed."""
+    P, B, width, pool, nsel = 16, 3, 800, 40, 3
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    blocks = B * width * P // 128
+    assert blocks * 2 * (H // 64) > sms
+    assert dsa.dsa_paged_attn_workspace_size(B, H, width, 0, P) == \
+        min(blocks, sms * 64 // H) * (2 * H * (4 * DV + 8) + 16)      # a unit per group of 64 heads
+    lens = [130, 1, 47]
+    table = torch.full((B, width), -1, dtype=torch.int32, device="cuda")
+    free, count, held, seq = i32(list(range(pool))), i32([pool]), i32([0] * B), i32(lens)
+    cache = torch.full((pool, P, D), NAN, dtype=torch.bfloat16, device="cuda")
+    keys = torch.zeros(pool, P, 128, dtype=torch.bfloat16, device="cuda")
+    means = torch.zeros(pool, 128, dtype=torch.bfloat16, device="cuda")
+    rows = [randn(n, D, seed=10 + b) for b, n in enumerate(lens)]
+    dsa.dsa_pages_update(table, held, seq, free, count, P)
+    slots = dsa.dsa_pages_slots(table, held, seq, P, sum(lens))
+    dsa.dsa_pages_append(torch.cat(rows).cuda(), randn(sum(lens), 128, seed=20).cuda(), slots, cache, keys, means)
+    held.copy_(seq)
+    kv, ki = torch.zeros(B, D, dtype=torch.bfloat16, device="cuda"), randn(B, 128, seed=21).cuda()
+    q, qi = torch.zeros(B, H, D, dtype=torch.bfloat16, device="cuda"), randn(B, 64, 128, seed=22).cuda()
+    w = torch.ones(B, 64, device="cuda")
+
+    def step():
+        seq.add_(1)
+        dsa.dsa_pages_update(table, held, seq, free, count, P)
+        dsa.dsa_pages_append(kv, ki, dsa.dsa_pages_slots(table, held, seq, P, B), cache, keys, means)
+        chosen = dsa.dsa_block_select(qi, w, means, table, seq, P, nsel)
+        held.copy_(seq)
+        return chosen, dsa.dsa_paged_attn(q, cache, table, seq, SCALE, DV, blocks=chosen), \
+            dsa.dsa_paged_attn(q, cache, table, seq, SCALE, DV)
+
+    graph = None
+    for t in range(20):
+        new = randn(B, D, seed=100 + t)
+        kv.copy_(new)
+        q.copy_(randn(B, H, D, seed=200 + t))
+        rows = [torch.cat([r, new[b:b + 1]]) for b, r in enumerate(rows)]
+        if t == 2:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                got = step()
+        if graph is None:
+            got = step()
+        else:
+            graph.replay()
+        now = [len(r) for r in rows]
+        wide = [r.cuda().double() for r in rows]
+        assert seq.tolist() == now
+        near(got[1], *attend64(q.cpu(), wide, now, blocks=got[0].tolist(), P=P))
+        near(got[2], *attend64(q.cpu(), wide, now))

@@ -377,3 +377,58 @@ def test_steps_over_a_wide_table(H):
         assert seq.tolist() == now
         near(got[1], *attend64(q.cpu(), wide, now, blocks=got[0].tolist(), P=P))
         near(got[2], *attend64(q.cpu(), wide, now))
+
+
+# ------------------------------------------------------------------ many queries, none, and rows of any width
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [2, 33])
+def test_many_more_queries_than_a_block_has_threads(H):
+    have, P, n = [60, 200], 32, 1500
+    cache, table, rows = paged(have, P, seed=H)
+    g = gen(8)
+    req = torch.randint(0, 2, (n,), generator=g).tolist()
+    lens = [int(torch.randint(-1, have[r] + 1, (1,), generator=g)) for r in req]
+    q = randn(n, H, D, seed=H)
+    out = torch.full((n, H, DV), 3.0, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_paged_attn(q.cuda(), cache, table, i32(lens), SCALE, DV, req=i32(req), out=out)
+    near(out, *attend64(q, rows, lens, req))
+    none = [i for i in range(n) if lens[i] < 0]
+    assert none and (out[none] == 3.0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H", [16, 128])
+def test_calls_without_any_query(H):
+    cache, table, _ = paged([100, 40], 16, seed=1)
+    q, out = randn(2, H, D, seed=2).cuda(), torch.full((2, H, DV), 3.0, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_paged_attn(q, cache, table, i32([-1, -2 ** 31]), SCALE, DV, out=out)
+    dsa.dsa_paged_attn(q, cache, table, i32([-1, -5]), SCALE, DV, blocks=i32([[0, 1], [0, 1]]), out=out)
+    assert (out == 3.0).all()
+    blocks = torch.full((2, 3), -9, dtype=torch.int32, device="cuda")
+    dsa.dsa_block_select(randn(2, 64, 128, seed=3).cuda(), torch.ones(2, 64, device="cuda"), randn(20, 128, seed=4).cuda(),
+                         table, i32([-1, -2 ** 31]), 16, 3, out=blocks)
+    assert (blocks == -9).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("width", [8, 760, 768, 776, 2000, 4096])
+@pytest.mark.parametrize("rows,DI", [(37, 8), (1100, 72)])
+def test_rows_of_any_width(width, rows, DI):
+    P, pages = 16, 80
+    kv, ki = randn(rows, width, seed=1).cuda(), randn(rows, DI, seed=2).cuda()
+    slots = torch.randperm(pages * P, generator=gen(width))[:rows].int().cuda()
+    cache = torch.zeros(pages, P, width, dtype=torch.bfloat16, device="cuda")
+    keys = torch.zeros(pages, P, DI, dtype=torch.bfloat16, device="cuda")
+    means = torch.full((pages, DI), 5.0, dtype=torch.bfloat16, device="cuda")
+    dsa.dsa_pages_append(kv, ki, slots, cache, keys, means)
+    want, want_keys = torch.zeros_like(cache), torch.zeros_like(keys)
+    want.view(-1, width)[slots.long()] = kv
+    want_keys.view(-1, DI)[slots.long()] = ki
+    assert torch.equal(cache, want) and torch.equal(keys, want_keys)
+    ended = torch.zeros(pages, dtype=torch.bool, device="cuda")
+    ended[slots[slots % P == P - 1].long() // P] = True
+    x = keys.double()
+    # half a step of bf16, and P fp32 additions
+    tol = 2.0 ** -8 * x.mean(1).abs() + 1.01 * P * 2.0 ** -24 * x.abs().mean(1)
+    assert ((means.double() - x.mean(1)).abs() <= tol)[ended].all() and (means[~ended] == 5.0).all()

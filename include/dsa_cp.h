@@ -712,8 +712,10 @@ dsa_status dsa_pages_append(const void *kv, int64_t kv_stride, const void *k_idx
  * A negative lens[i] is no query: its row of blocks keeps its values.  A request
  * or length that the table does not have, and a page number that is none, are
  * DSA_ERR_DEVICE_BOUNDS (such a page ranks last, behind NaN scores, but is taken
- * where it is one of the first and last ones or all are).  A query's scores are kept in
- * shared memory: max_pages up to 37,000 (DSA_ERR_UNSUPPORTED beyond).
+ * where it is one of the first and last ones or all are).  A query's scores are
+ * kept in shared memory: max_pages up to 37,000 (DSA_ERR_UNSUPPORTED beyond).
+ * Many queries of a request share the reading of its keys only where max_pages <=
+ * 4,096, however short the request is.
  */
 dsa_status dsa_block_select(const void *q_idx, const float *w, int32_t n, int32_t HI, int32_t DI,
                             const void *block_keys, int32_t num_pages, int32_t page_size, const int32_t *page_table,
@@ -749,7 +751,9 @@ dsa_status dsa_paged_attn_workspace_size(int32_t n, int32_t H, int32_t max_pages
  * softmax_scale > 0 and finite.  bf16 products with fp32 sums, softmax in fp32
  * but for the weights that multiply the values (bf16, each within 2^-8 of
  * itself).  The work is divided by the lengths, on the device, and parts are
- * joined in a fixed order: the same inputs give the same bits.
+ * joined in a fixed order: the same inputs give the same bits.  How many SMs few
+ * short queries get is decided by max_pages: a table no wider than the requests
+ * need is fastest for them.
  */
 dsa_status dsa_paged_attn(const void *q, int32_t n, const void *cache, int64_t page_stride, int64_t row_stride,
                           int32_t num_pages, int32_t page_size, const int32_t *page_table, int32_t batch,

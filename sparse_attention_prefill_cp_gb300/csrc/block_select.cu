@@ -18,9 +18,9 @@
 // What bounds it: a group of four queries and 1,024 pages takes 29 K cycles, of
 // them 2 K to set up, 4 K to the first tile's MMA, 1.7 K a tile in the sums (1,024
 // of MMA; a weight read from shared memory by a warp is 128 bytes into registers,
-// 1,024 cycles a tile where none are held: 64 us against 61, and maxima run at half
+// 1,024 cycles a tile where none are held: 64 us against 60, and maxima run at half
 // rate) and 8 K for the choice; a CTA fills an SM, so nothing hides start and
-// choice.  2,048 queries of 1,024 pages 61 us, 565 TFLOP/s; 64 requests 10.5 us.
+// choice.  2,048 queries of 1,024 pages 60.4 us, 569 TFLOP/s; 64 requests 10.6 us.
 #include "attn_common.cuh"
 #include "internal.h"
 
@@ -50,9 +50,9 @@ struct SelCfg {
   static constexpr int kBufs = 2;                   // accumulators
   static constexpr int kSumWarps = QT == 1 ? 8 : 16, kTeamWarps = kSumWarps / QT;
   static constexpr int kMmaWarp = kSumWarps, kFirstLoadWarp = kMmaWarp + 1;
-  static constexpr int kLoadWarps = QT == 1 ? 4 : 2;     // 19 warps leave a thread 96 registers, for most of its weights
+  static constexpr int kLoadWarps = QT == 1 ? 4 : 2;     // 19 warps leave a thread 96 registers
   static constexpr int kRead = QT == 1 ? 32 : 16;        // columns of an accumulator at a time
-  static constexpr int kHeldWeights = QT == 1 ? 0 : 48;  // of a query's 64 in registers, the others read for every tile
+  static constexpr int kHeldWeights = QT == 1 ? 0 : 48;  // of a query's 64 in registers (8 bytes spill), the others read
   static constexpr int kThreads = 32 * (kFirstLoadWarp + kLoadWarps);
   static constexpr int kOffQ = kStages * kTileBytes;
   static constexpr int kQChunk = N * 128;
@@ -558,7 +558,10 @@ extern "C" dsa_status dsa_block_select(const void *q_idx, const float *w, int32_
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   // four queries share a request's keys where queries may share requests and there are more than fit the SMs at once,
   // two CTAs of a query to an SM (625 blocks: 304 queries 13.5 against 12.1 us, 400 13.5 against 21.4); where there are
-  // no more queries than SMs a longer ring instead of a second CTA (64 of 1,024 blocks: 10.5 against 11.5 us)
+  // no more queries than SMs a longer ring instead of a second CTA (64 of 1,024 blocks: 10.5 against 11.5 us).  All by
+  // the table's width, since lengths are on the device: the scores of four queries fit beside the rest up to 4,096
+  // pages, and in a wider table each query gathers its request's keys alone (600 queries of 4,096 pages 47 us, of
+  // 4,097 82), however short the requests are
   if (req && n > 2 * num_sms() && smem_bytes<SelCfg<4, 3>>(max_pages) <= kMaxSmem) return launch<SelCfg<4, 3>>(P, s);
   if (n <= num_sms() && smem_bytes<SelCfg<1, 4>>(max_pages) <= kMaxSmem) return launch<SelCfg<1, 4>>(P, s);
   return launch<SelCfg<1, 2>>(P, s);

@@ -40,7 +40,7 @@
 // block of 64 heads moves 578 KB (operands of QK and PV 415, TMA 147, P 16), 4,520
 // cycles, and takes 5,850, since Q and one block fill the 227 KB and nothing of the
 // next lands while the softmax runs: 64 requests of 8,192 rows 189 us, 2,048 queries
-// of 2,048 rows 1,384 us, 844 TFLOP/s.
+// of 2,048 rows 1,390 us, 840 TFLOP/s.
 #include "internal.h"
 #include "paged_attn.cuh"
 
@@ -106,7 +106,7 @@ __device__ __forceinline__ bool wg_or(int wg, bool p) {
 
 // A plain load that stays where it stands: what the compiler makes of a[i] here it
 // may also move or repeat, and the kernel of 64 heads then spills 12 bytes (chunk of
-// 2,048 queries: 1,394 against 1,384 us).
+// 2,048 queries: 1,394 against 1,385 us).
 __device__ __forceinline__ int load_plain(const int32_t *p) {
   int x;
   asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(p));
@@ -687,7 +687,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 // group as can be, since each group reads the rows; but where every block can have
 // an SM for each of smaller groups, those, whose block is shorter (one token of 128
 // heads over 1,024 rows: groups of 64 17.2 us, of 32 13.8, of 16 13.9; of 64 heads,
-// 16 requests of 128 rows: 12.6 against 10.7).
+// 16 requests of 128 rows: 12.6 against 10.7).  Lengths are on the device, so the
+// blocks are those of a full table: a wide table keeps the large groups however short
+// the requests are.  Heads that a group lacks cost what they would if they were there
+// (64 x 8,192 rows: 96 heads 186 us, 128 189).
 struct PagedDivision {
   int group_heads, groups, units;
 };

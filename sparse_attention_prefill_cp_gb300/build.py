@@ -131,7 +131,12 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         if force or _stale(obj, [src] + headers):
             procs.append((src, _start([nvcc()] + NVCC_FLAGS + SOURCE_FLAGS.get(os.path.basename(src), []) +
                                       list(extra_flags) + ["-c", src, "-o", obj], verbose)))
-    binding = compile_binding(verbose, force) if importlib.util.find_spec("torch") is not None else None
+    binding, fault = None, None
+    try:
+        if importlib.util.find_spec("torch") is not None:
+            binding = compile_binding(verbose, force)
+    except Exception as e:  # raised when the library is there
+        fault = e
     try:
         _finish(procs, verbose)
         if force or procs or _stale(LIB_PATH, objs):
@@ -141,6 +146,8 @@ def build(verbose: bool = False, force: bool = False, extra_flags=()) -> str:
         for _, p in binding or []:
             p.communicate()
         raise
+    if fault is not None:
+        raise fault
     if binding is not None:
         link_binding(binding, verbose, force)
     return LIB_PATH

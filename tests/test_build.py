@@ -62,6 +62,18 @@ def test_a_tree_without_torch_builds_the_library(tree, monkeypatch):
     assert (pkg / "libdsa_cp.so").exists() and not list(pkg.glob("_binding*"))
 
 
+def test_a_torch_that_cannot_be_imported_spoils_the_binding_alone(tree, monkeypatch):
+    pkg, _, _ = tree
+
+    def tag():
+        raise ImportError("no such library")
+
+    monkeypatch.setattr(B, "binding_tag", tag)
+    with pytest.raises(ImportError, match="no such library"):
+        B.build()
+    assert (pkg / "libdsa_cp.so").exists()
+
+
 def test_the_librarys_faults_are_raised(tree):
     pkg, _, refused = tree
     refused.add("b.cu")
